@@ -2,7 +2,7 @@
 
 Each .cu under csrc/ is compiled with nvcc to an object under _build/, then
 linked into cross_layer_kv_shared_b200/libkvshare.so. Objects are rebuilt when
-their source or any header is newer. Usage: python -m cross_layer_kv_shared_b200.build
+their source or a header they include (as nvcc recorded it) is newer. Usage: python -m cross_layer_kv_shared_b200.build
 """
 from __future__ import annotations
 
@@ -30,12 +30,22 @@ def _headers():
         glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
+def _included(obj: str):
+    """The repository's headers an object was compiled from (its .d file), or every header without one."""
+    if not os.path.exists(obj + ".d"):
+        return _headers()
+    with open(obj + ".d") as f:
+        names = f.read().partition(" : ")[2].replace("\\\n", " ").split()
+    return [n for n in names if os.path.abspath(n).startswith(ROOT + os.sep)]
+
+
 def _compile(src: str, extra=()) -> str:
     obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-    newest = max([os.path.getmtime(src)] + [os.path.getmtime(h) for h in _headers()])
+    deps = [src] + _included(obj)
+    newest = max(os.path.getmtime(d) if os.path.exists(d) else float("inf") for d in deps)
     if os.path.exists(obj) and os.path.getmtime(obj) >= newest and not extra:
         return obj
-    cmd = [NVCC, *ARCH, *FLAGS, *extra, "-c", src, "-o", obj]
+    cmd = [NVCC, *ARCH, *FLAGS, *extra, "-MD", "-MF", obj + ".d", "-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
