@@ -12,6 +12,7 @@ namespace kvs {
 // bits of the device status word
 constexpr unsigned ERR_TIMEOUT = 1u;
 constexpr unsigned ERR_RANGE = 2u;     // a per-sequence length outside [0, context] (clamped)
+constexpr unsigned ERR_POOL = 4u;      // the paged cache's pool had fewer free pages than requested
 
 // one split partial: o[d] (un-normalised, relative to m), m (log2 domain), l
 constexpr int MAX_SPLITS = 160;

@@ -43,6 +43,13 @@ class kvshare_cache(ctypes.Structure):
                 ("lengths", ctypes.c_void_p)]
 
 
+class kvshare_pages(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("bound_codes", ctypes.c_void_p),
+                ("bound_scale", ctypes.c_void_p), ("slots", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("block_table", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
+                ("batch", ctypes.c_int), ("max_blocks", ctypes.c_int)]
+
+
 class KVShareError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -64,6 +71,11 @@ def _load():
         "kvshare_prefill": ([P, ctypes.POINTER(kvshare_cache), P, P, P, I, I, I, V], I),
         "kvshare_pack_residual": ([P, P, P, P, P, P, P, P, P, I, I, V], I),
         "kvshare_append_lowrank": ([P, ctypes.POINTER(kvshare_cache), P, P, P, P, V], I),
+        "kvshare_plan_pages": ([P] * 11 + [I, I, I, I, I, V], I),
+        "kvshare_append_paged": ([P, ctypes.POINTER(kvshare_pages), I, P, P, ctypes.c_longlong, ctypes.c_longlong, P,
+                                  I, V], I),
+        "kvshare_decode_paged": ([P, ctypes.POINTER(kvshare_pages), P, P, P, P, I, I, I, V], I),
+        "kvshare_select_pages": ([P, ctypes.POINTER(kvshare_pages), P, P, I, I, I, I, I, V], I),
         "kvshare_sync_status": ([P, V], I),
         "kvshare_set_splits": ([P, I], I),
         "kvshare_set_kv_overlap": ([P, I], I),
@@ -107,6 +119,11 @@ def _stream(stream) -> Optional[int]:
     return int(getattr(stream, "cuda_stream", stream))
 
 
+# (query heads, (kv heads, head dim), torch type) of each live context: what the paged entry
+# points check their tensors against
+_configs = {}
+
+
 def kvshare_create(num_layers: int, num_q_heads: int, num_kv_heads: int, head_dim: int, dtype: int,
                    max_batch: int, max_context: int, softmax_scale: float = 0.0, basis_rank: int = 32,
                    max_resid_rank: int = 16, check: bool = True):
@@ -117,10 +134,13 @@ def kvshare_create(num_layers: int, num_q_heads: int, num_kv_heads: int, head_di
     st = _lib.kvshare_create(ctypes.byref(cfg), ctypes.byref(h))
     if check:
         _check(st, "kvshare_create")
+    if st == KVS_OK:
+        _configs[h.value] = (num_q_heads, (num_kv_heads, head_dim), "torch.float32" if dtype == KVS_F32 else "torch.bfloat16")
     return st, h
 
 
 def kvshare_destroy(h) -> int:
+    _configs.pop(getattr(h, "value", h), None)
     return _lib.kvshare_destroy(h)
 
 
@@ -225,6 +245,134 @@ def kvshare_append_lowrank(h, cache: Cache, k_new, v_new, score, pos, stream=Non
                                      _stream(stream))
     if check:
         _check(st, "kvshare_append_lowrank")
+    return st
+
+
+# ---- paged cache. A pool's sizes are not known to the C side, so these entry points check
+# their tensors' shapes, types and strides here (EINVAL) before the call.
+def _is(t, dtype: str, *shape) -> bool:
+    """A dense CUDA tensor of the named torch type; None in `shape` takes any size."""
+    return t is not None and t.is_cuda and str(t.dtype) == "torch." + dtype and t.is_contiguous() and \
+        len(t.shape) == len(shape) and all(b is None or a == b for a, b in zip(t.shape, shape))
+
+
+@dataclass(frozen=True)
+class Pages:
+    """Device tensors of a paged cache (fields as in kvshare_pages); sizes are the tensors' own.
+
+    k, v [slots][num_pages][Hkv][page_size][d]; block_table [batch][max_blocks] int32;
+    lengths [batch] int32; bound_codes [slots][num_pages][Hkv][2][d] int8 and bound_scale
+    [slots][num_pages][Hkv] float32 where block selection is used. The tensors' contents may
+    change between calls, the tensors may not (make another Pages for others).
+    """
+    k: object
+    v: object
+    block_table: object
+    lengths: object
+    bound_codes: object = None
+    bound_scale: object = None
+
+    def __post_init__(self):
+        k, v, t = self.k, self.v, self.block_table
+        name = str(k.dtype).replace("torch.", "")
+        ok = name in ("bfloat16", "float32") and len(k.shape) == 5 and _is(k, name, *k.shape) and \
+            _is(v, name, *k.shape) and _is(t, "int32", None, None) and _is(self.lengths, "int32", t.shape[0])
+        if self.bound_codes is not None or self.bound_scale is not None:
+            ok = ok and _is(self.bound_codes, "int8", *k.shape[:3], 2, k.shape[4]) and \
+                _is(self.bound_scale, "float32", *k.shape[:3])
+        if not ok:
+            raise KVShareError(KVS_EINVAL, "Pages")
+        c = kvshare_pages(_ptr(k), _ptr(v), _ptr(self.bound_codes), _ptr(self.bound_scale), k.shape[0], k.shape[1],
+                          k.shape[3], _ptr(t), _ptr(self.lengths), t.shape[0], t.shape[1])
+        object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "_ref", ctypes.byref(c))
+        object.__setattr__(self, "_heads", (k.shape[2], k.shape[4]))
+        object.__setattr__(self, "_dtype", k.dtype)
+
+
+def _fits(h, pages: Pages) -> bool:
+    """The pool's heads, width and type are the context's."""
+    cfg = _configs.get(h.value)
+    return cfg is not None and pages._heads == cfg[1] and str(pages._dtype) == cfg[2]
+
+
+def _rows(t, dtype, layers: int, batch: int, *rest) -> bool:
+    """A dense CUDA tensor [>= layers][batch]...: the layer-major arrays of a decode."""
+    return t.is_cuda and t.dtype == dtype and t.is_contiguous() and t.shape[0] >= layers and \
+        t.shape[1:] == (batch, *rest)
+
+
+def kvshare_plan_pages(h, lengths, new_tokens, block_table, ring, ring_state, lengths_out, ring_state_out,
+                       token_start, slot_map, position, page_size: int, stream=None, check: bool = True) -> int:
+    ok = all(_is(t, "int32", *([None] * len(t.shape))) for t in (block_table, ring, slot_map)) and \
+        len(block_table.shape) == 2 and len(ring.shape) == 1 and len(slot_map.shape) == 1
+    if ok:
+        B, M = block_table.shape[0], slot_map.shape[0]
+        ok = _is(lengths, "int32", B) and _is(new_tokens, "int32", B) and _is(lengths_out, "int32", B) and \
+            _is(ring_state, "int32", 2) and _is(ring_state_out, "int32", 2) and _is(token_start, "int32", B + 1) and \
+            _is(position, "int32", M)
+    st = KVS_EINVAL if not ok else _lib.kvshare_plan_pages(
+        h, lengths.data_ptr(), new_tokens.data_ptr(), block_table.data_ptr(), ring.data_ptr(), ring_state.data_ptr(),
+        lengths_out.data_ptr(), ring_state_out.data_ptr(), token_start.data_ptr(), slot_map.data_ptr(),
+        position.data_ptr(), B, block_table.shape[1], int(page_size), ring.shape[0], M, _stream(stream))
+    if check:
+        _check(st, "kvshare_plan_pages")
+    return st
+
+
+def kvshare_append_paged(h, pages: Pages, slot: int, k_new, v_new, slot_map, stream=None, check: bool = True) -> int:
+    """k_new, v_new: [tokens][Hkv][d], each token's heads dense; the tokens may be rows of a wider tensor."""
+    n = slot_map.shape[0]
+    H, d = pages._heads
+    ok = _fits(h, pages) and _is(slot_map, "int32", n)
+    for t in (k_new, v_new):
+        ok = ok and t.is_cuda and t.dtype == pages._dtype and t.shape == (n, H, d) and \
+            (n == 0 or t.stride()[1:] == (d, 1) or (H == 1 and t.stride(2) == 1))
+    # a single token's stride says nothing about its row
+    row = lambda t: t.stride(0) if n > 1 else H * d  # noqa: E731
+    st = KVS_EINVAL if not ok else _lib.kvshare_append_paged(
+        h, pages._ref, int(slot), k_new.data_ptr(), v_new.data_ptr(), row(k_new), row(v_new), slot_map.data_ptr(), n,
+        _stream(stream))
+    if check:
+        _check(st, "kvshare_append_paged")
+    return st
+
+
+def kvshare_decode_paged(h, pages: Pages, q, out, lse=None, l0: int = 0, l1: int = None, selected=None, stream=None,
+                         check: bool = True) -> int:
+    import torch
+    l1 = q.shape[0] if l1 is None else int(l1)
+    ok = _fits(h, pages)
+    top = 0
+    if ok:
+        (H, d), B, Hq = pages._heads, pages._c.batch, _configs[h.value][0]
+        ok = _rows(q, pages._dtype, l1, B, Hq, d) and _rows(out, torch.float32, l1, B, Hq, d) and \
+            (lse is None or _rows(lse, torch.float32, l1, B, Hq))
+        if selected is not None:
+            top = selected.shape[-1]
+            # an empty list has no address, which would ask for every block
+            ok = ok and top > 0 and _rows(selected, torch.int32, l1, B, H, top)
+    st = KVS_EINVAL if not ok else _lib.kvshare_decode_paged(
+        h, pages._ref, q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+        None if selected is None else selected.data_ptr(), top, int(l0), l1, _stream(stream))
+    if check:
+        _check(st, "kvshare_decode_paged")
+    return st
+
+
+def kvshare_select_pages(h, pages: Pages, q, selected, first: int = 1, last: int = 1, l0: int = 0, l1: int = None,
+                         stream=None, check: bool = True) -> int:
+    import torch
+    l1 = q.shape[0] if l1 is None else int(l1)
+    top = selected.shape[-1]
+    ok = _fits(h, pages)
+    if ok:
+        (H, d), B, Hq = pages._heads, pages._c.batch, _configs[h.value][0]
+        ok = _rows(q, pages._dtype, l1, B, Hq, d) and _rows(selected, torch.int32, l1, B, H, top)
+    st = KVS_EINVAL if not ok else _lib.kvshare_select_pages(
+        h, pages._ref, q.data_ptr(), selected.data_ptr(), top, int(first), int(last), int(l0), l1, _stream(stream))
+    if check:
+        _check(st, "kvshare_select_pages")
     return st
 
 

@@ -58,7 +58,7 @@ typedef enum {
     KVS_OK = 0,
     KVS_EINVAL = 1,        /* bad argument: null/misaligned pointer, shape, map entry, range */
     KVS_EUNSUPPORTED = 2,  /* valid but not implemented (head_dim, dtype/kind combination)   */
-    KVS_ENOMEM = 3,        /* device allocation failed in kvshare_create                      */
+    KVS_ENOMEM = 3,        /* device allocation failed; from sync_status: a page pool ran out */
     KVS_ECUDA = 4,         /* a CUDA runtime call failed                                      */
     KVS_ETIMEOUT = 5       /* a device-side bounded wait ran out (reported by sync_status)    */
 } kvshare_status;
@@ -125,6 +125,35 @@ typedef struct {
                               kvshare_sync_status return KVS_EINVAL. NULL: every
                               sequence has T tokens. Prefill takes NULL only. */
 } kvshare_cache;
+
+/* A paged shared cache (forms SINGLE and MIX): the tokens of a sequence lie in pages of
+ * page_size tokens anywhere in a pool, in the order its row of the block table names them.
+ * Token t of sequence b is row t % page_size of page block_table[b][t / page_size], in every
+ * slot. The page tables of the systems that serve such models are what lets a batch of
+ * growing requests share one memory ("A Systematic Study of Cross-Layer KV Sharing for
+ * Efficient LLM Inference", TL;DR: throughput at large batch sizes); a slot is shared by
+ * layers exactly as a dense store's is.
+ * block_table and lengths are read on the device: a length outside [0, max_blocks *
+ * page_size] is clamped, a page outside [0, num_pages) reads as zeros and is never written,
+ * and either makes the next kvshare_sync_status return KVS_EINVAL. Block-table entries past
+ * a sequence's last block are not read. Tokens past its length may hold anything (NaN).
+ * num_pages * page_size and slots * num_pages * Hkv must stay below 2^31; byte offsets are
+ * 64-bit. batch <= max_batch and (max_blocks - 1) * page_size < max_context of the context. */
+typedef struct {
+    const void* k;             /* [slots][num_pages][Hkv][page_size][d] dtype of the config   */
+    const void* v;
+    const int8_t* bound_codes; /* [slots][num_pages][Hkv][2][d] key bounds of each page, upper
+                                  then lower, or NULL (block selection needs them)            */
+    const float* bound_scale;  /* [slots][num_pages][Hkv]: bound = scale * code               */
+    int slots;
+    int num_pages;
+    int page_size;             /* 16, 32, 64, 128 or 256                                      */
+    const int* block_table;    /* [batch][max_blocks] int32 DEVICE                            */
+    const int* lengths;        /* [batch] int32 DEVICE: tokens of each sequence, the new one
+                                  included                                                    */
+    int batch;
+    int max_blocks;
+} kvshare_pages;
 
 /* Create a context on the current CUDA device. Allocates the split workspace
  * (sized by max_batch / max_context) and a device status word. `out` receives
@@ -269,9 +298,87 @@ kvshare_status kvshare_pack_residual(kvshare_t ctx, const float* score, const fl
 kvshare_status kvshare_append_lowrank(kvshare_t ctx, const kvshare_cache* cache, const void* k_new,
                                       const void* v_new, const float* score, const int* pos, void* stream);
 
+/* Pages and slots of one step of a paged cache, planned on the GPU from the sequences'
+ * lengths, so that a captured step needs no host. All arrays are int32 DEVICE arrays.
+ *   lengths     [batch] cached tokens n_b
+ *   new_tokens  [batch] tokens m_b sequence b takes now; m_b < 0: the sequence leaves
+ *   block_table [batch][max_blocks], in place: entries of new blocks are written
+ *   ring        [num_pages] free pages, in place: `count` of them from entry `head` on,
+ *               modulo num_pages; ring_state = {head, count}
+ *   lengths_out [batch]: n_b + m_b, or 0 for a sequence that leaves
+ *   ring_state_out [2]; token_start [batch + 1]: first new token of each sequence, then
+ *               their total
+ *   slot_map, position [max_tokens]: for new token i, sequences end to end, its slot
+ *               page * page_size + row and its position in its sequence; past the last
+ *               token -1 and 0
+ * New pages are taken from the ring's head in (sequence, block) order. Pages of sequences
+ * that leave go behind its last entry in that order and are free from the next call on;
+ * their block-table rows are left as they were. Sequence b is admitted iff the pages
+ * that 0 .. b need fit the free ones (or it needs none) and the tokens that 0 .. b ask
+ * for fit max_tokens; otherwise it takes nothing (length unchanged) and the next
+ * kvshare_sync_status returns KVS_ENOMEM. A sequence that would pass max_blocks *
+ * page_size takes nothing, and more returning pages than the pool has room for are
+ * dropped; both report KVS_EINVAL. lengths_out may be lengths and ring_state_out
+ * ring_state; no other two arrays may overlap. A page belongs to one sequence at a time.
+ * batch <= 4096 (KVS_EUNSUPPORTED above), batch * max_blocks and max_blocks * page_size
+ * below 2^31. */
+kvshare_status kvshare_plan_pages(kvshare_t ctx, const int* lengths, const int* new_tokens, int* block_table,
+                                  int* ring, const int* ring_state, int* lengths_out, int* ring_state_out,
+                                  int* token_start, int* slot_map, int* position, int batch, int max_blocks,
+                                  int page_size, int num_pages, int max_tokens, void* stream);
+
+/* Write new tokens into one slot of a paged cache, in place.
+ *   k_new, v_new: token i, kv head j at element i * stride + j * d (config dtype; strides
+ *                 in elements, multiples of 16 bytes, at least Hkv * d: rows may be read
+ *                 out of a wider projection)
+ *   slot_map:     [tokens] int32 DEVICE; token i goes to row slot_map[i] % page_size of page
+ *                 slot_map[i] / page_size; an entry < 0 is skipped, one past the pool is
+ *                 skipped and makes the next kvshare_sync_status return KVS_EINVAL
+ * With pages.bound_codes, the key bounds of every page written to are made again from its
+ * rows 0 .. the last one written here: per channel the largest and the smallest key,
+ * rounded outwards to int8 with one fp32 scale per page and head (max |bound| * (1/127),
+ * the reciprocal in fp32; codes ceil(hi / scale), floor(lo / scale) clamped to +-127). Keys
+ * must be finite then. The tokens of one page must be consecutive, in row order (as
+ * kvshare_plan_pages lays them out), and no slot may appear twice.
+ * pages.block_table and lengths are not read. A decode that follows on the same stream
+ * sees the new tokens. */
+kvshare_status kvshare_append_paged(kvshare_t ctx, const kvshare_pages* pages, int slot, const void* k_new,
+                                    const void* v_new, long long k_stride, long long v_stride,
+                                    const int* slot_map, int tokens, void* stream);
+
+/* kvshare_decode over a paged cache, layers [l0, l1), one kernel per layer.
+ *   q, out, lse: as in kvshare_decode (lse may be NULL)
+ *   selected:    [L][batch][Hkv][top] int32 DEVICE block indices to attend to, as written by
+ *                kvshare_select_pages (distinct; the first min(top, blocks of b) entries of a
+ *                row are read, in any order; one outside the sequence's blocks is skipped
+ *                and reported as KVS_EINVAL), or NULL: every block
+ * Sequences of any mix of lengths share the GPU evenly: the split is computed on the
+ * device from the lengths, and the joins run in a fixed order, so the same inputs give the
+ * same bits. Attention weights enter the P.V product with 24 bits: results differ from
+ * exact arithmetic by fp32 rounding only. A sequence of length 0 gets out 0 and lse -inf.
+ * LOWRANK layers: KVS_EUNSUPPORTED (their code groups are not paged). */
+kvshare_status kvshare_decode_paged(kvshare_t ctx, const kvshare_pages* pages, const void* q, float* out,
+                                    float* lse, const int* selected, int top, int l0, int l1, void* stream);
+
+/* Choose the blocks a sparse decode attends to, layers [l0, l1): for every (sequence, kv
+ * head) the `first` first blocks, the `last` last ones and those with the highest score, in
+ * ascending order, min(top, blocks) of them and then -1; ties go to the lowest block.
+ *   selected: [L][batch][Hkv][top] int32 DEVICE
+ * The score of a page bounds q . k over its keys from above, in int8: with q's codes c =
+ * rint(q / s_q), s_q = max |q| * (1/127) per head, dot = sum_c (c > 0 ? c hi : c lo) over the
+ * page's bound codes and score = (dot * s_q) * bound_scale, each step one fp32 operation;
+ * for a MIX layer w * score_1 + (1 - w) * score_2; the largest over the group's heads.
+ * Selections are reproducible bit for bit. 0 <= first, 1 <= last, first + last <= top,
+ * max_blocks <= 16384 (KVS_EUNSUPPORTED above). Layers that share a source may share a
+ * selection. */
+kvshare_status kvshare_select_pages(kvshare_t ctx, const kvshare_pages* pages, const void* q, int* selected,
+                                    int top, int first, int last, int l0, int l1, void* stream);
+
 /* Synchronise `stream`, then read and clear the device status word.
  * Returns KVS_OK, KVS_ETIMEOUT (a bounded device wait ran out), KVS_EINVAL (a
- * per-sequence length outside [0, context] was clamped) or KVS_ECUDA. */
+ * per-sequence length outside [0, context] was clamped, or an index outside a paged
+ * cache was skipped), KVS_ENOMEM (kvshare_plan_pages did not admit a sequence) or
+ * KVS_ECUDA. */
 kvshare_status kvshare_sync_status(kvshare_t ctx, void* stream);
 
 /* Split-KV override for decode: 0 = automatic (default), n > 0 = n splits per

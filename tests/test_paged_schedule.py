@@ -1,0 +1,61 @@
+"""The paged decode's split, modelled on the CPU: every tile has one warp, and the CTAs a unit's
+join waits for are exactly those that hold a part of it (a mismatch would leave a partial
+unjoined, or an arrival counter that never returns to zero)."""
+import random
+
+import pytest
+
+
+def shares(W, nw, ctas):
+    nc = min(ctas, max(1, -(-W // nw)))
+    workers = nc * nw
+    return nc, workers, [(W * i // workers, W * (i + 1) // workers) for i in range(workers)]
+
+
+def owner(x, W, workers):
+    return ((x + 1) * workers - 1) // W
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_join_counts_match_the_shares(seed):
+    r = random.Random(seed)
+    nw = r.choice([2, 4, 8])
+    ctas = r.choice([1, 3, 17, 148])
+    heads = r.choice([1, 2, 5, 8])
+    tiles = [r.choice([0, 1, 2, 3, r.randrange(0, 40), r.randrange(0, 3000)]) for _ in range(r.randrange(1, 30))]
+    units = [t for t in tiles for _ in range(heads) if t]
+    W = sum(units)
+    if W == 0:
+        return
+    nc, workers, parts = shares(W, nw, ctas)
+    assert parts[0][0] == 0 and parts[-1][1] == W and all(a[1] == b[0] for a, b in zip(parts, parts[1:]))
+    # every CTA holds a tile, so none between a unit's first and last is missing
+    assert all(parts[c * nw][0] < parts[c * nw + nw - 1][1] for c in range(nc))
+    begin = 0
+    slots = set()
+    for n in units:
+        first, last = owner(begin, W, workers), owner(begin + n - 1, W, workers)
+        assert parts[first][0] <= begin < parts[first][1]
+        assert parts[last][0] <= begin + n - 1 < parts[last][1]
+        holders = {i // nw for i, (a, b) in enumerate(parts) if a < begin + n and b > begin}
+        assert holders == set(range(first // nw, last // nw + 1))
+        if first // nw != last // nw:
+            # one slot per partial: a CTA begins at most one unit it does not end
+            mine = {2 * c + (1 if c == first // nw else 0) for c in holders}
+            assert not mine & slots
+            slots |= mine
+        begin += n
+    assert all(s < 2 * ctas for s in slots)
+
+
+def test_windows_of_page_entries_cover_a_tile():
+    # 32 entries from a tile's first block: the tile's later pieces stay inside the window
+    for page, tile in ((16, 16), (16, 32), (32, 32), (64, 32), (128, 16), (256, 32)):
+        for start in range(0, 200):
+            base = None
+            for t in range(start, start + 200):
+                blk = t * tile // page
+                if base is None or blk >= base + 32:
+                    base = blk
+                pieces = {(t * tile + r) // page - base for r in range(0, tile, min(page, tile))}
+                assert min(pieces) >= 0 and max(pieces) <= 31
