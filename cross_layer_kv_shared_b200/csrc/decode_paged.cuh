@@ -27,7 +27,7 @@
 
 namespace kvs {
 
-constexpr int PAGED_SMEM_MAX = 232448 - 4096;   // dynamic share of an SM's 227 KB (static beside it)
+constexpr int PAGED_SMEM_MAX = 232448 - 7168;   // dynamic share of an SM's 227 KB (static beside it)
 
 // Zero rows [r0, r1) of a staged tile: `subs` blocks of `sub_stride` bytes, 128 bytes a row.
 __device__ __forceinline__ void zero_rows(uint8_t* base, int subs, int sub_stride, int r0, int r1, int lane) {
@@ -36,6 +36,9 @@ __device__ __forceinline__ void zero_rows(uint8_t* base, int subs, int sub_strid
         *reinterpret_cast<uint4*>(base + (i / per) * sub_stride + (r0 + (i % per) / 8) * 128 + (i % 8) * 16) =
             make_uint4(0u, 0u, 0u, 0u);
 }
+
+// 1 / l; 0 where no token was attended to
+__device__ __forceinline__ float inverse_of(float l) { return l > 0.f ? 1.f / l : 0.f; }
 
 // P: the arithmetic of one storage type (see PagedBf16, PagedF32). It fixes D, NSRC, TT, NH
 // (padded heads), NW (warps), NSW (stages), SUBW (elements of a 128-byte row), STAGE (bytes)
@@ -54,7 +57,7 @@ struct PagedLayout {
 };
 
 struct PagedState {
-    int unit;       // b * Hkv + j, or -1
+    int head0;      // the unit's first query head, b * Hq + j * g, or -1: no state
     int begin;      // the unit's first tile on the line
     int tiles;      // its tiles
     int started;    // the unit's first tile is in this state
@@ -77,6 +80,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     __shared__ int s_lim[NW * NSW * BLK];
     __shared__ PagedState s_state[NW * 2];
     __shared__ float s_m[NW * 2][NH], s_l[NW * 2][NH];
+    __shared__ int s_part[2][3];                 // units that continue elsewhere: first head, first CTA, CTAs
     __shared__ unsigned s_last[2];
 
     const int cta = blockIdx.x;
@@ -91,7 +95,8 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         for (int i = 0; i < NW * NSW; ++i) mbar_init(&bars[i], 1);
         mbar_init_fence();
     }
-    if (threadIdx.x < NW * 2) s_state[threadIdx.x].unit = -1;
+    if (threadIdx.x < NW * 2) s_state[threadIdx.x].head0 = -1;
+    if (threadIdx.x < 2) s_part[threadIdx.x][0] = -1;
     __syncthreads();
     grid_dep_wait();
     if (threadIdx.x == 0) grid_dep_launch();
@@ -113,48 +118,46 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     auto row_tiles = [&](int n) {
         return ((a.sel != nullptr ? row_blocks(n) << a.page_shift : n) + TT - 1) / TT;
     };
-    int total = 0;
-    for (int b = lane; b < a.B; b += 32) total += row_tiles(row_len(b));
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
-    const long long W = static_cast<long long>(total) * a.Hkv;
+    // 32-bit arithmetic: the caller keeps the line below 2^31 tiles
+    const int n_lane = lane < a.B ? row_len(lane) : 0;       // the first 32 sequences, one per lane
+    const int tiles_lane = row_tiles(n_lane);
+    unsigned total = tiles_lane;
+    for (int b = lane + 32; b < a.B; b += 32) total += row_tiles(row_len(b));
+    const unsigned W = __reduce_add_sync(0xffffffffu, total) * a.Hkv;
     // no more CTAs than tiles: every CTA between a unit's first and last holds a part of it
-    const int nc = static_cast<int>(min(static_cast<long long>(a.ctas), max(1LL, (W + NW - 1) / NW)));
-    const int workers = nc * NW;
-    long long t0 = 0, t1 = 0;
-    if (cta < nc) {
-        t0 = W * (cta * NW + warp) / workers;
-        t1 = W * (cta * NW + warp + 1) / workers;
-    }
-    const int my_n = static_cast<int>(t1 - t0);
+    const unsigned nc = max(1u, min(static_cast<unsigned>(a.ctas), (W + NW - 1) / NW));
+    const unsigned workers = nc * NW, share = W / workers, more = W - share * workers;
+    const unsigned id = cta * NW + warp;         // the first `more` warps take one tile more
+    const unsigned t0 = share * id + min(id, more);
+    const int my_n = id < workers ? share + (id < more ? 1 : 0) : 0;
 
     struct Cursor {
         int b, j, t, n, tiles;
     };
     Cursor at = {0, 0, 0, 0, 0};
     if (my_n > 0) {
-        long long base = 0;
+        unsigned base = 0;
         for (int r0 = 0; r0 < a.B; r0 += 32) {
-            const int n = r0 + lane < a.B ? row_len(r0 + lane) : 0;
-            const int own = row_tiles(n);
-            long long incl = static_cast<long long>(own) * a.Hkv;
+            const int n = r0 == 0 ? n_lane : r0 + lane < a.B ? row_len(r0 + lane) : 0;
+            const int own = r0 == 0 ? tiles_lane : row_tiles(n);
+            unsigned incl = static_cast<unsigned>(own) * a.Hkv;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
-                const long long x = __shfl_up_sync(0xffffffffu, incl, off);
+                const unsigned x = __shfl_up_sync(0xffffffffu, incl, off);
                 if (lane >= off) incl += x;
             }
-            const long long all = __shfl_sync(0xffffffffu, incl, 31);
-            if (t0 < base + all) {
-                const int who = __ffs(__ballot_sync(0xffffffffu, base + incl > t0)) - 1;
+            const unsigned ahead = __ballot_sync(0xffffffffu, base + incl > t0);
+            if (ahead != 0u) {
+                const int who = __ffs(ahead) - 1;
                 at.b = r0 + who;
                 at.n = __shfl_sync(0xffffffffu, n, who);
                 at.tiles = __shfl_sync(0xffffffffu, own, who);
-                const long long row0 = base + __shfl_sync(0xffffffffu, incl, who) - static_cast<long long>(at.tiles) * a.Hkv;
-                at.j = static_cast<int>((t0 - row0) / at.tiles);
-                at.t = static_cast<int>((t0 - row0) % at.tiles);
+                const unsigned in_row = t0 - (base + __shfl_sync(0xffffffffu, incl, who) - static_cast<unsigned>(at.tiles) * a.Hkv);
+                at.j = in_row / at.tiles;
+                at.t = in_row - at.j * at.tiles;
                 break;
             }
-            base += all;
+            base += __shfl_sync(0xffffffffu, incl, 31);
         }
     }
     // to the next unit that has tiles (only called while the share holds more)
@@ -198,6 +201,15 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         }
         wvalid = true;
     };
+    // one lane per copy: piece of the tile, sub-tile, K or V, source
+    constexpr int PB = SUBS * 2 * P::NSRC;       // copies of one page piece
+    static_assert(PB * (TT > 16 ? 2 : 1) <= 32, "one lane per copy");
+    const int pc_r = (lane / PB) * rows;         // this lane's piece starts at token pc_r of a tile
+    const int pc_h = lane % SUBS;
+    const int pc_side = (lane % PB) / SUBS;      // K, V (, K, V of the second source)
+    const CUtensorMap* pc_map = (pc_side & 1) ? &tmV : &tmK;
+    const int pc_slot = ((pc_side >> 1) ? a.src1 : a.src0) * a.num_pages;
+    const int pc_off = pc_side * TILE_BYTES + pc_h * SUB_BYTES + pc_r * 128;
     auto issue = [&](int k) {
         if (ic.t == ic.tiles) {
             next_unit(ic);
@@ -207,30 +219,15 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         const int blk = tok >> a.page_shift;
         if (!wvalid || blk >= wbase + 32) load_window(blk);
         const int s = k % NSW;
-        uint8_t* st = ring + s * P::STAGE;
+        // lane i looks up the piece it copies; lanes below BLK also the limit of block i
+        const int phys = __shfl_sync(0xffffffffu, wphys, (((tok + pc_r) >> a.page_shift) - wbase) & 31);
+        const int lim_tok = tok + (lane % BLK) * 16;
+        const int lg = __shfl_sync(0xffffffffu, wlog, (lim_tok >> a.page_shift) - wbase);
+        if (lane < BLK) lims[s * BLK + lane] = lg < 0 ? 0 : ic.n - (lg << a.page_shift) - (lim_tok & (ps - 1));
         if (lane == 0) mbar_arrive_expect_tx(&wb[s], P::STAGE);
-        for (int r = 0; r < TT; r += rows) {
-            const int in_page = (tok + r) & (ps - 1);
-            const int from = ((tok + r) >> a.page_shift) - wbase;
-            const int phys = __shfl_sync(0xffffffffu, wphys, from);
-            const int lg = __shfl_sync(0xffffffffu, wlog, from);
-            if (lane == 0) {
-                const int lim = lg < 0 ? 0 : ic.n - (lg << a.page_shift) - in_page;
-                for (int i = 0; i < rows / 16; ++i) lims[s * BLK + r / 16 + i] = lim - 16 * i;
-                const int c0 = phys < 0 ? -1 : (a.src0 * a.num_pages + phys) * a.Hkv + ic.j;
-                const int c1 = phys < 0 ? -1 : (a.src1 * a.num_pages + phys) * a.Hkv + ic.j;
-#pragma unroll
-                for (int h = 0; h < SUBS; ++h) {
-                    uint8_t* dst = st + h * SUB_BYTES + r * 128;
-                    tma_load_3d(dst, &tmK, h * P::SUBW, in_page, c0, &wb[s]);
-                    tma_load_3d(dst + TILE_BYTES, &tmV, h * P::SUBW, in_page, c0, &wb[s]);
-                    if (P::NSRC == 2) {
-                        tma_load_3d(dst + 2 * TILE_BYTES, &tmK, h * P::SUBW, in_page, c1, &wb[s]);
-                        tma_load_3d(dst + 3 * TILE_BYTES, &tmV, h * P::SUBW, in_page, c1, &wb[s]);
-                    }
-                }
-            }
-        }
+        if (pc_r < TT)
+            tma_load_3d(ring + s * P::STAGE + pc_off, pc_map, pc_h * P::SUBW, (tok + pc_r) & (ps - 1),
+                        phys < 0 ? -1 : (pc_slot + phys) * a.Hkv + ic.j, &wb[s]);
         ++ic.t;
         __syncwarp();
     };
@@ -254,9 +251,9 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     auto end_unit = [&](int k) {
         p.finish();
         const bool started = first_tile == 0, ended = cc.t == cc.tiles;
-        const size_t head0 = static_cast<size_t>(cc.b) * a.Hq + static_cast<size_t>(cc.j) * g;
+        const int head0 = cc.b * a.Hq + cc.j * g;
         if (started && ended) {
-            p.each(g, [&](int h, int e, float v, float l) { a.out[(head0 + h) * D + e] = l > 0.f ? v / l : 0.f; });
+            p.each(g, [&](int h, int e, float v, float inv) { a.out[static_cast<size_t>(head0 + h) * D + e] = v * inv; });
             if (a.lse != nullptr) p.stats(g, [&](int h, float m, float l) { a.lse[head0 + h] = lse_of(m, l); });
             return;
         }
@@ -268,7 +265,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             s_l[which][h] = l;
         });
         if (lane == 0)
-            s_state[which] = {cc.b * a.Hkv + cc.j, static_cast<int>(t0 + k) - cc.t, cc.tiles, started ? 1 : 0, ended ? 1 : 0};
+            s_state[which] = {head0, static_cast<int>(t0) + k - cc.t, cc.tiles, started ? 1 : 0, ended ? 1 : 0};
     };
     if (my_n > 0) p.begin(a, cc.b, cc.j);
     for (int k = 0; k < my_n; ++k) {
@@ -307,128 +304,138 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     if (my_n > 0) end_unit(my_n);
     __syncthreads();
 
-    // ---- join the warps' states, unit by unit (states are in the line's order)
-    const float* saved = reinterpret_cast<const float*>(smem + L::RING);
-    auto state_o = [&](int i) {
-        return (i & 1) ? reinterpret_cast<const float*>(smem + (i >> 1) * NSW * P::STAGE) : saved + (i >> 1) * NH * D;
+    // ---- join the warps' states, unit by unit. States are in the line's order; every warp
+    // finds the units' first states by votes (lane i: state i)
+    int unit_l = -1, flags_l = 0;
+    PagedState mine = {-1, 0, 0, 0, 0};
+    if (lane < 2 * NW) mine = s_state[lane];
+    unit_l = mine.head0;
+    flags_l = mine.started | mine.ended << 1;
+    const unsigned valid = __ballot_sync(0xffffffffu, unit_l >= 0);
+    const unsigned below = valid & ((1u << lane) - 1u);
+    const int prev = __shfl_sync(0xffffffffu, unit_l, below ? 31 - __clz(below) : lane);
+    const unsigned firsts = __ballot_sync(0xffffffffu, unit_l >= 0 && (below == 0u || prev != unit_l));
+    // states of the unit that begins at state i: those up to the next unit's first
+    auto states_from = [&](int i) {
+        const unsigned later = firsts & ~((2u << i) - 1u);
+        return valid & ~((1u << i) - 1u) & (later ? (later & (0u - later)) - 1u : 0xffffffffu);
     };
-    // a unit that continues in other CTAs: [0] began earlier, [1] goes on later
-    int part_unit[2] = {-1, -1}, part_c0[2] = {0, 0}, part_n[2] = {0, 0};
+    // the last state of this lane's unit says whether the unit ends here
+    const unsigned own_states = (firsts >> lane) & 1u ? states_from(lane) : 0u;
+    const int last_flags = __shfl_sync(0xffffffffu, flags_l, own_states ? 31 - __clz(own_states) : lane);
+    const bool split = own_states != 0u && !((flags_l & 1) && (last_flags & 2));
+    const unsigned splits = __ballot_sync(0xffffffffu, split);
+    if (split && warp == 0) {
+        // the CTA whose share holds a tile
+        auto owner = [&](unsigned x) {
+            const unsigned big = more * (share + 1);
+            return static_cast<int>((x < big ? x / (share + 1) : more + (x - big) / share) / NW);
+        };
+        int* part = s_part[flags_l & 1];
+        part[0] = unit_l;
+        part[1] = owner(mine.begin);
+        part[2] = owner(mine.begin + mine.tiles - 1) - part[1] + 1;
+    }
     const int per = paged_partial(g, D);
-    for (int i = 0; i < 2 * NW;) {
-        const int unit = s_state[i].unit;
-        if (unit < 0) {
-            ++i;
-            continue;
+    const int items = g * (D / 4), groups = __popc(firsts);
+    for (int k = threadIdx.x; k < groups * items; k += NW * 32) {
+        const int idx = k % items;
+        unsigned rest = firsts;
+        for (int c = k / items; c > 0; --c) rest &= rest - 1u;
+        const int i = __ffs(rest) - 1;
+        const unsigned states = states_from(i);
+        const int h = idx / (D / 4), e = (idx % (D / 4)) * 4;
+        float M = NEG_INF;
+#pragma unroll
+        for (int s = 0; s < 2 * NW; ++s)
+            if ((states >> s) & 1u) M = fmaxf(M, s_m[s][h]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
+#pragma unroll
+        for (int s = 0; s < 2 * NW; ++s) {
+            if (!((states >> s) & 1u)) continue;
+            const float f = merge_factor(s_m[s][h], M);
+            // odd states lie over their warp's ring, even ones in the save area
+            const float4 v = *reinterpret_cast<const float4*>(
+                smem + ((s & 1) ? (s >> 1) * NSW * P::STAGE : L::RING + (s >> 1) * NH * D * 4) + (h * D + e) * 4);
+            l = fmaf(f, s_l[s][h], l);
+            acc.x = fmaf(f, v.x, acc.x);
+            acc.y = fmaf(f, v.y, acc.y);
+            acc.z = fmaf(f, v.z, acc.z);
+            acc.w = fmaf(f, v.w, acc.w);
         }
-        int last = i, i1 = i + 1;
-        for (; i1 < 2 * NW && (s_state[i1].unit < 0 || s_state[i1].unit == unit); ++i1)
-            if (s_state[i1].unit == unit) last = i1;
-        const bool started = s_state[i].started, ended = s_state[last].ended;
-        const bool whole = started && ended;
-        const int which = started ? 1 : 0;
-        float* part = a.ws + static_cast<size_t>(2 * cta + which) * per;
-        if (!whole) {
-            // CTA of a tile: the worker with the largest index whose share begins at or before it
-            const long long x0 = s_state[i].begin, x1 = x0 + s_state[i].tiles - 1;
-            const int c0 = static_cast<int>(((x0 + 1) * workers - 1) / W) / NW;
-            const int c1 = static_cast<int>(((x1 + 1) * workers - 1) / W) / NW;
-            part_unit[which] = unit;
-            part_c0[which] = c0;
-            part_n[which] = c1 - c0 + 1;
+        if ((splits >> i) & 1u) {
+            float* part = a.ws + static_cast<size_t>(2 * cta + s_state[i].started) * per;
+            *reinterpret_cast<float4*>(part + h * D + e) = acc;
+            if (e == 0) *reinterpret_cast<float2*>(part + g * D + 2 * h) = make_float2(M, l);
+        } else {
+            const int head = s_state[i].head0 + h;
+            const float inv = inverse_of(l);
+            *reinterpret_cast<float4*>(a.out + static_cast<size_t>(head) * D + e) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+            if (e == 0 && a.lse != nullptr) a.lse[head] = lse_of(M, l);
         }
-        const size_t head0 = static_cast<size_t>(unit / a.Hkv) * a.Hq + static_cast<size_t>(unit % a.Hkv) * g;
-        for (int idx = threadIdx.x; idx < g * (D / 4); idx += NW * 32) {
-            const int h = idx / (D / 4), e = (idx % (D / 4)) * 4;
-            float M = NEG_INF;
-            for (int s = i; s <= last; ++s)
-                if (s_state[s].unit == unit) M = fmaxf(M, s_m[s][h]);
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            float l = 0.f;
-            for (int s = i; s <= last; ++s) {
-                if (s_state[s].unit != unit) continue;
-                const float f = merge_factor(s_m[s][h], M);
-                const float4 v = *reinterpret_cast<const float4*>(state_o(s) + h * D + e);
-                l = fmaf(f, s_l[s][h], l);
-                acc.x = fmaf(f, v.x, acc.x);
-                acc.y = fmaf(f, v.y, acc.y);
-                acc.z = fmaf(f, v.z, acc.z);
-                acc.w = fmaf(f, v.w, acc.w);
-            }
-            if (whole) {
-                float* o = a.out + (head0 + h) * D + e;
-                *reinterpret_cast<float4*>(o) = l > 0.f ? make_float4(acc.x / l, acc.y / l, acc.z / l, acc.w / l)
-                                                        : make_float4(0.f, 0.f, 0.f, 0.f);
-                if (e == 0 && a.lse != nullptr) a.lse[head0 + h] = lse_of(M, l);
-            } else {
-                *reinterpret_cast<float4*>(part + h * D + e) = acc;
-                if (e == 0) {
-                    part[g * D + h] = M;
-                    part[g * D + g + h] = l;
-                }
-            }
-        }
-        i = i1;
     }
-    if (part_unit[0] < 0 && part_unit[1] < 0) return;
+    if (splits == 0u) return;
 
-    // ---- the last CTA of a unit to arrive joins its partials
-    __threadfence();
+    // ---- the last CTA of a unit to arrive joins its partials. Its thread's acq_rel atomic,
+    // between two block barriers, orders every thread's partial before it and every read after it
     __syncthreads();
-    if (threadIdx.x < 2 && part_unit[threadIdx.x] >= 0) {
-        const int c0 = threadIdx.x == 0 ? part_c0[0] : part_c0[1];
-        const int n = threadIdx.x == 0 ? part_n[0] : part_n[1];
-        unsigned prev;
-        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(prev) : "l"(a.counters + c0) : "memory");
-        s_last[threadIdx.x] = prev == static_cast<unsigned>(n - 1) ? 1u : 0u;
+    if (threadIdx.x < 2 && s_part[threadIdx.x][0] >= 0) {
+        unsigned prev_n;
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
+                     : "=r"(prev_n)
+                     : "l"(a.counters + s_part[threadIdx.x][1])
+                     : "memory");
+        s_last[threadIdx.x] = prev_n == static_cast<unsigned>(s_part[threadIdx.x][2] - 1) ? 1u : 0u;
     }
     __syncthreads();
-    float* fac = reinterpret_cast<float*>(smem);         // [n][g] m, then the factors
+    float2* stat = reinterpret_cast<float2*>(smem);      // [n][g] (m, l), over the ring
     for (int which = 0; which < 2; ++which) {
-        const int unit = which == 0 ? part_unit[0] : part_unit[1];
-        if (unit < 0 || s_last[which] == 0u) continue;   // the same for every thread
-        const int c0 = which == 0 ? part_c0[0] : part_c0[1];
-        const int n = which == 0 ? part_n[0] : part_n[1];
-        __threadfence();
+        const int head0 = s_part[which][0];
+        if (head0 < 0 || s_last[which] == 0u) continue;  // the same for every thread
+        const int c0 = s_part[which][1], n = s_part[which][2];
         // partial i: CTA c0 + i, which began the unit (slot 1) or continued it (slot 0)
-        auto slot = [&](int i) { return a.ws + static_cast<size_t>(2 * (c0 + i) + (i == 0 ? 1 : 0)) * per; };
-        float* sum = fac + n * g;                        // [g] M, [g] l
-        for (int idx = threadIdx.x; idx < n * g; idx += NW * 32) fac[idx] = __ldcg(slot(idx / g) + g * D + idx % g);
-        __syncthreads();
-        for (int h = warp; h < g; h += NW) {
-            float M = NEG_INF;
-            for (int i = lane; i < n; i += 32) M = fmaxf(M, fac[i * g + h]);
-            M = warp_max(M);
-            float l = 0.f;
-            for (int i = lane; i < n; i += 32) {
-                const float f = merge_factor(fac[i * g + h], M);
-                fac[i * g + h] = f;
-                l = fmaf(f, __ldcg(slot(i) + g * D + g + h), l);
-            }
-            l = warp_sum(l);
-            if (lane == 0) {
-                sum[h] = M;
-                sum[g + h] = l;
-            }
+        const float* base = a.ws + static_cast<size_t>(2 * c0) * per;
+        auto slot = [&](int i) { return base + (2 * i + (i == 0 ? 1 : 0)) * per; };
+        // a thread's first values are on their way while the statistics are shared
+        constexpr int AHEAD = 4;
+        const int h0 = threadIdx.x / (D / 4), e0 = (threadIdx.x % (D / 4)) * 4;
+        float4 v0[AHEAD];
+        if (threadIdx.x < items) {
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                if (i < n) v0[i] = __ldcg(reinterpret_cast<const float4*>(slot(i) + h0 * D + e0));
         }
+        for (int i = warp; i < n; i += NW)
+            if (lane < g) stat[i * g + lane] = __ldcg(reinterpret_cast<const float2*>(slot(i) + g * D) + lane);
         __syncthreads();
-        const size_t head0 = static_cast<size_t>(unit / a.Hkv) * a.Hq + static_cast<size_t>(unit % a.Hkv) * g;
-        for (int idx = threadIdx.x; idx < g * (D / 4); idx += NW * 32) {
+        for (int idx = threadIdx.x; idx < items; idx += NW * 32) {
             const int h = idx / (D / 4), e = (idx % (D / 4)) * 4;
+            float M = NEG_INF;
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) M = fmaxf(M, stat[i * g + h].x);
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int i = 0; i < n; ++i) {
-                const float f = fac[i * g + h];
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(slot(i) + h * D + e));
+            float l = 0.f;
+            auto add = [&](int i, const float4& v) {
+                const float2 ml = stat[i * g + h];
+                const float f = merge_factor(ml.x, M);
+                l = fmaf(f, ml.y, l);
                 acc.x = fmaf(f, v.x, acc.x);
                 acc.y = fmaf(f, v.y, acc.y);
                 acc.z = fmaf(f, v.z, acc.z);
                 acc.w = fmaf(f, v.w, acc.w);
+            };
+            int i = 0;
+            if (idx == threadIdx.x) {
+#pragma unroll
+                for (; i < AHEAD; ++i)
+                    if (i < n) add(i, v0[i]);
             }
-            const float l = sum[g + h];
-            *reinterpret_cast<float4*>(a.out + (head0 + h) * D + e) =
-                l > 0.f ? make_float4(acc.x / l, acc.y / l, acc.z / l, acc.w / l) : make_float4(0.f, 0.f, 0.f, 0.f);
-            if (e == 0 && a.lse != nullptr) a.lse[head0 + h] = lse_of(sum[h], l);
+#pragma unroll 4
+            for (; i < n; ++i) add(i, __ldcg(reinterpret_cast<const float4*>(slot(i) + h * D + e)));
+            const float inv = inverse_of(l);
+            *reinterpret_cast<float4*>(a.out + static_cast<size_t>(head0 + h) * D + e) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+            if (e == 0 && a.lse != nullptr) a.lse[head0 + h] = lse_of(M, l);
         }
         if (threadIdx.x == 0) a.counters[c0] = 0u;
         __syncthreads();

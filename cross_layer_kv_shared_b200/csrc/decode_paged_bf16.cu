@@ -186,17 +186,20 @@ struct PagedBf16 {
             }
     }
 
+    // f(head, channel, value, 1 / l) for what this lane holds of the unit
     template <typename F>
     __device__ void each(int g, F f) {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        for (int nb = 0; nb < NB; ++nb) {
+            const float inv[2] = {inverse_of(l[nb][0]), inverse_of(l[nb][1])};
 #pragma unroll
             for (int dt = 0; dt < D / 16; ++dt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int h = nb * 8 + 2 * (lane & 3) + (i & 1);
-                    if (h < g) f(h, dt * 16 + (lane >> 2) + (i >> 1) * 8, o[dt][nb][i], l[nb][i & 1]);
+                    if (h < g) f(h, dt * 16 + (lane >> 2) + (i >> 1) * 8, o[dt][nb][i], inv[i & 1]);
                 }
+        }
     }
 
     template <typename F>

@@ -191,19 +191,20 @@ struct PagedF32 {
         __syncwarp();
         if ((lane & 7) == 0)
 #pragma unroll
-            for (int h = 0; h < HQ; ++h) sc[(lane >> 3) * HQ + h] = l[h];
+            for (int h = 0; h < HQ; ++h) sc[(lane >> 3) * HQ + h] = inverse_of(l[h]);
         __syncwarp();
     }
 
+    // f(head, channel, value, 1 / l) for what this lane holds of the unit
     template <typename F>
     __device__ void each(int g, F f) {
         if (lane >= EL) return;
 #pragma unroll
         for (int h = 0; h < NH; ++h)
             if (h < g) {
-                const float lh = sc[h];
+                const float inv = sc[h];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) f(h, lane * 4 + x, o[h][x], lh);
+                for (int x = 0; x < 4; ++x) f(h, lane * 4 + x, o[h][x], inv);
             }
     }
 

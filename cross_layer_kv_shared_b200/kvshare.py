@@ -119,8 +119,8 @@ def _stream(stream) -> Optional[int]:
     return int(getattr(stream, "cuda_stream", stream))
 
 
-# (query heads, (kv heads, head dim), torch type) of each live context: what the paged entry
-# points check their tensors against
+# (query heads, (kv heads, head dim, dtype)) of each live context: what the paged entry points
+# check their tensors against
 _configs = {}
 
 
@@ -135,7 +135,7 @@ def kvshare_create(num_layers: int, num_q_heads: int, num_kv_heads: int, head_di
     if check:
         _check(st, "kvshare_create")
     if st == KVS_OK:
-        _configs[h.value] = (num_q_heads, (num_kv_heads, head_dim), "torch.float32" if dtype == KVS_F32 else "torch.bfloat16")
+        _configs[h.value] = (num_q_heads, (num_kv_heads, head_dim, dtype))
     return st, h
 
 
@@ -249,11 +249,21 @@ def kvshare_append_lowrank(h, cache: Cache, k_new, v_new, score, pos, stream=Non
 
 
 # ---- paged cache. A pool's sizes are not known to the C side, so these entry points check
-# their tensors' shapes, types and strides here (EINVAL) before the call.
-def _is(t, dtype: str, *shape) -> bool:
-    """A dense CUDA tensor of the named torch type; None in `shape` takes any size."""
-    return t is not None and t.is_cuda and str(t.dtype) == "torch." + dtype and t.is_contiguous() and \
-        len(t.shape) == len(shape) and all(b is None or a == b for a, b in zip(t.shape, shape))
+# their tensors' shapes, types and strides here (EINVAL) before the call; that the memory is
+# the context's device's is checked there.
+_TYPES = {}     # torch type -> kvshare_dtype, filled with the first Pages
+
+
+def _dense(t, dtype, shape) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous()
+
+
+def _device_stream(stream, t) -> Optional[int]:
+    """The given stream, or torch's current one on the tensor's own device."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return int(getattr(stream, "cuda_stream", stream))
 
 
 @dataclass(frozen=True)
@@ -273,48 +283,50 @@ class Pages:
     bound_scale: object = None
 
     def __post_init__(self):
-        k, v, t = self.k, self.v, self.block_table
-        name = str(k.dtype).replace("torch.", "")
-        ok = name in ("bfloat16", "float32") and len(k.shape) == 5 and _is(k, name, *k.shape) and \
-            _is(v, name, *k.shape) and _is(t, "int32", None, None) and _is(self.lengths, "int32", t.shape[0])
+        import torch
+        _TYPES.update({torch.bfloat16: KVS_BF16, torch.float32: KVS_F32})
+        k, t = self.k, self.block_table
+        ok = k.dtype in _TYPES and k.dim() == 5 and t.dim() == 2
+        ok = ok and _dense(k, k.dtype, k.shape) and _dense(self.v, k.dtype, k.shape) and \
+            _dense(t, torch.int32, t.shape) and _dense(self.lengths, torch.int32, (t.shape[0],))
         if self.bound_codes is not None or self.bound_scale is not None:
-            ok = ok and _is(self.bound_codes, "int8", *k.shape[:3], 2, k.shape[4]) and \
-                _is(self.bound_scale, "float32", *k.shape[:3])
-        if not ok:
+            ok = ok and self.bound_codes is not None and self.bound_scale is not None and \
+                _dense(self.bound_codes, torch.int8, (*k.shape[:3], 2, k.shape[4])) and \
+                _dense(self.bound_scale, torch.float32, k.shape[:3])
+        used = [x for x in (k, self.v, t, self.lengths, self.bound_codes, self.bound_scale) if x is not None]
+        if not ok or not all(x.is_cuda and x.get_device() == k.get_device() for x in used):
             raise KVShareError(KVS_EINVAL, "Pages")
-        c = kvshare_pages(_ptr(k), _ptr(v), _ptr(self.bound_codes), _ptr(self.bound_scale), k.shape[0], k.shape[1],
-                          k.shape[3], _ptr(t), _ptr(self.lengths), t.shape[0], t.shape[1])
-        object.__setattr__(self, "_c", c)
-        object.__setattr__(self, "_ref", ctypes.byref(c))
-        object.__setattr__(self, "_heads", (k.shape[2], k.shape[4]))
-        object.__setattr__(self, "_dtype", k.dtype)
+        c = kvshare_pages(_ptr(k), _ptr(self.v), _ptr(self.bound_codes), _ptr(self.bound_scale), k.shape[0],
+                          k.shape[1], k.shape[3], _ptr(t), _ptr(self.lengths), t.shape[0], t.shape[1])
+        keep = lambda name, x: object.__setattr__(self, name, x)  # noqa: E731
+        keep("_c", c)
+        keep("_ref", ctypes.byref(c))
+        # what a context must have been created with
+        keep("_model", (k.shape[2], k.shape[4], _TYPES[k.dtype]))
 
 
-def _fits(h, pages: Pages) -> bool:
-    """The pool's heads, width and type are the context's."""
-    cfg = _configs.get(h.value)
-    return cfg is not None and pages._heads == cfg[1] and str(pages._dtype) == cfg[2]
-
-
-def _rows(t, dtype, layers: int, batch: int, *rest) -> bool:
-    """A dense CUDA tensor [>= layers][batch]...: the layer-major arrays of a decode."""
-    return t.is_cuda and t.dtype == dtype and t.is_contiguous() and t.shape[0] >= layers and \
-        t.shape[1:] == (batch, *rest)
+def _layer_range(pages: Pages, cfg, q, l1):
+    """(query shape [L][batch][Hq][d] expected, l1), or None if q does not hold layers up to l1."""
+    L = q.shape[0] if q.dim() == 4 else 0
+    l1 = L if l1 is None else int(l1)
+    shape = (L, pages._c.batch, cfg[0], cfg[1][1])
+    return (shape, l1) if 0 <= l1 <= L and _dense(q, pages.k.dtype, shape) else None
 
 
 def kvshare_plan_pages(h, lengths, new_tokens, block_table, ring, ring_state, lengths_out, ring_state_out,
                        token_start, slot_map, position, page_size: int, stream=None, check: bool = True) -> int:
-    ok = all(_is(t, "int32", *([None] * len(t.shape))) for t in (block_table, ring, slot_map)) and \
-        len(block_table.shape) == 2 and len(ring.shape) == 1 and len(slot_map.shape) == 1
-    if ok:
-        B, M = block_table.shape[0], slot_map.shape[0]
-        ok = _is(lengths, "int32", B) and _is(new_tokens, "int32", B) and _is(lengths_out, "int32", B) and \
-            _is(ring_state, "int32", 2) and _is(ring_state_out, "int32", 2) and _is(token_start, "int32", B + 1) and \
-            _is(position, "int32", M)
-    st = KVS_EINVAL if not ok else _lib.kvshare_plan_pages(
-        h, lengths.data_ptr(), new_tokens.data_ptr(), block_table.data_ptr(), ring.data_ptr(), ring_state.data_ptr(),
-        lengths_out.data_ptr(), ring_state_out.data_ptr(), token_start.data_ptr(), slot_map.data_ptr(),
-        position.data_ptr(), B, block_table.shape[1], int(page_size), ring.shape[0], M, _stream(stream))
+    from torch import int32
+    st = KVS_EINVAL
+    if block_table.dim() == 2 and ring.dim() == 1 and slot_map.dim() == 1:
+        (B, P), N, M = block_table.shape, ring.shape[0], slot_map.shape[0]
+        if _dense(block_table, int32, (B, P)) and _dense(ring, int32, (N,)) and _dense(slot_map, int32, (M,)) and \
+                _dense(position, int32, (M,)) and _dense(lengths, int32, (B,)) and _dense(new_tokens, int32, (B,)) and \
+                _dense(lengths_out, int32, (B,)) and _dense(ring_state, int32, (2,)) and \
+                _dense(ring_state_out, int32, (2,)) and _dense(token_start, int32, (B + 1,)) and lengths.is_cuda:
+            st = _lib.kvshare_plan_pages(
+                h, lengths.data_ptr(), new_tokens.data_ptr(), block_table.data_ptr(), ring.data_ptr(),
+                ring_state.data_ptr(), lengths_out.data_ptr(), ring_state_out.data_ptr(), token_start.data_ptr(),
+                slot_map.data_ptr(), position.data_ptr(), B, P, page_size, N, M, _device_stream(stream, lengths))
     if check:
         _check(st, "kvshare_plan_pages")
     return st
@@ -322,17 +334,19 @@ def kvshare_plan_pages(h, lengths, new_tokens, block_table, ring, ring_state, le
 
 def kvshare_append_paged(h, pages: Pages, slot: int, k_new, v_new, slot_map, stream=None, check: bool = True) -> int:
     """k_new, v_new: [tokens][Hkv][d], each token's heads dense; the tokens may be rows of a wider tensor."""
-    n = slot_map.shape[0]
-    H, d = pages._heads
-    ok = _fits(h, pages) and _is(slot_map, "int32", n)
-    for t in (k_new, v_new):
-        ok = ok and t.is_cuda and t.dtype == pages._dtype and t.shape == (n, H, d) and \
-            (n == 0 or t.stride()[1:] == (d, 1) or (H == 1 and t.stride(2) == 1))
-    # a single token's stride says nothing about its row
-    row = lambda t: t.stride(0) if n > 1 else H * d  # noqa: E731
-    st = KVS_EINVAL if not ok else _lib.kvshare_append_paged(
-        h, pages._ref, int(slot), k_new.data_ptr(), v_new.data_ptr(), row(k_new), row(v_new), slot_map.data_ptr(), n,
-        _stream(stream))
+    from torch import int32
+    st, cfg = KVS_EINVAL, _configs.get(h.value)
+    if cfg is not None and cfg[1] == pages._model and slot_map.dim() == 1:
+        n, (H, d, _) = slot_map.shape[0], pages._model
+        dt, shape = pages.k.dtype, (n, H, d)
+        if _dense(slot_map, int32, (n,)) and k_new.dtype is dt and v_new.dtype is dt and k_new.shape == shape and \
+                v_new.shape == shape:
+            (kr, kh, ke), (vr, vh, ve) = k_new.stride(), v_new.stride()
+            if ke == 1 and ve == 1 and (H == 1 or (kh == d and vh == d)):
+                if n <= 1:                      # one token's stride says nothing about its row
+                    kr = vr = H * d
+                st = _lib.kvshare_append_paged(h, pages._ref, slot, k_new.data_ptr(), v_new.data_ptr(), kr, vr,
+                                               slot_map.data_ptr(), n, _device_stream(stream, pages.k))
     if check:
         _check(st, "kvshare_append_paged")
     return st
@@ -340,21 +354,22 @@ def kvshare_append_paged(h, pages: Pages, slot: int, k_new, v_new, slot_map, str
 
 def kvshare_decode_paged(h, pages: Pages, q, out, lse=None, l0: int = 0, l1: int = None, selected=None, stream=None,
                          check: bool = True) -> int:
-    import torch
-    l1 = q.shape[0] if l1 is None else int(l1)
-    ok = _fits(h, pages)
-    top = 0
-    if ok:
-        (H, d), B, Hq = pages._heads, pages._c.batch, _configs[h.value][0]
-        ok = _rows(q, pages._dtype, l1, B, Hq, d) and _rows(out, torch.float32, l1, B, Hq, d) and \
-            (lse is None or _rows(lse, torch.float32, l1, B, Hq))
+    from torch import float32, int32
+    st, cfg = KVS_EINVAL, _configs.get(h.value)
+    got = _layer_range(pages, cfg, q, l1) if cfg is not None and cfg[1] == pages._model else None
+    if got is not None:
+        shape, l1 = got
+        ok = _dense(out, float32, shape) and (lse is None or _dense(lse, float32, shape[:3]))
+        top = 0
         if selected is not None:
-            top = selected.shape[-1]
             # an empty list has no address, which would ask for every block
-            ok = ok and top > 0 and _rows(selected, torch.int32, l1, B, H, top)
-    st = KVS_EINVAL if not ok else _lib.kvshare_decode_paged(
-        h, pages._ref, q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
-        None if selected is None else selected.data_ptr(), top, int(l0), l1, _stream(stream))
+            top = selected.shape[-1]
+            ok = ok and top > 0 and _dense(selected, int32, (*shape[:2], pages._model[0], top))
+        if ok:
+            st = _lib.kvshare_decode_paged(h, pages._ref, q.data_ptr(), out.data_ptr(),
+                                           None if lse is None else lse.data_ptr(),
+                                           None if selected is None else selected.data_ptr(), top, l0, l1,
+                                           _device_stream(stream, pages.k))
     if check:
         _check(st, "kvshare_decode_paged")
     return st
@@ -362,15 +377,15 @@ def kvshare_decode_paged(h, pages: Pages, q, out, lse=None, l0: int = 0, l1: int
 
 def kvshare_select_pages(h, pages: Pages, q, selected, first: int = 1, last: int = 1, l0: int = 0, l1: int = None,
                          stream=None, check: bool = True) -> int:
-    import torch
-    l1 = q.shape[0] if l1 is None else int(l1)
-    top = selected.shape[-1]
-    ok = _fits(h, pages)
-    if ok:
-        (H, d), B, Hq = pages._heads, pages._c.batch, _configs[h.value][0]
-        ok = _rows(q, pages._dtype, l1, B, Hq, d) and _rows(selected, torch.int32, l1, B, H, top)
-    st = KVS_EINVAL if not ok else _lib.kvshare_select_pages(
-        h, pages._ref, q.data_ptr(), selected.data_ptr(), top, int(first), int(last), int(l0), l1, _stream(stream))
+    from torch import int32
+    st, cfg = KVS_EINVAL, _configs.get(h.value)
+    got = _layer_range(pages, cfg, q, l1) if cfg is not None and cfg[1] == pages._model else None
+    if got is not None:
+        shape, l1 = got
+        top = selected.shape[-1]
+        if _dense(selected, int32, (*shape[:2], pages._model[0], top)):
+            st = _lib.kvshare_select_pages(h, pages._ref, q.data_ptr(), selected.data_ptr(), top, first, last, l0, l1,
+                                           _device_stream(stream, pages.k))
     if check:
         _check(st, "kvshare_select_pages")
     return st

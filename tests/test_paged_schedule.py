@@ -7,13 +7,16 @@ import pytest
 
 
 def shares(W, nw, ctas):
-    nc = min(ctas, max(1, -(-W // nw)))
+    nc = max(1, min(ctas, -(-W // nw)))
     workers = nc * nw
-    return nc, workers, [(W * i // workers, W * (i + 1) // workers) for i in range(workers)]
+    share, more = divmod(W, workers)
+    return nc, workers, [(share * i + min(i, more), share * (i + 1) + min(i + 1, more)) for i in range(workers)]
 
 
 def owner(x, W, workers):
-    return ((x + 1) * workers - 1) // W
+    share, more = divmod(W, workers)
+    big = more * (share + 1)
+    return x // (share + 1) if x < big else more + (x - big) // share
 
 
 @pytest.mark.parametrize("seed", range(40))
