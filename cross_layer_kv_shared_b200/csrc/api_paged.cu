@@ -77,19 +77,20 @@ kvshare_status check_layers(const kvshare_ctx* c, const kvshare_pages* p, int l0
     return KVS_OK;
 }
 
-// [rows][page][d] of a pool, boxes of `box_rows` tokens and 128 bytes, 128-byte swizzle
+// [rows][page][d] of a pool as [rows][128-byte column block][page][columns]: a box of
+// `box_rows` tokens and every column block lands in shared memory block by block, each
+// 128-byte swizzled, in one copy
 bool pool_map(const kvshare_ctx* c, const kvshare_pages* p, const void* base, int box_rows, CUtensorMap* out) {
     EncodeTiledFn fn = encode_fn();
     if (fn == nullptr) return false;
     const bool f32 = c->cfg.dtype == KVS_F32;
-    const cuuint64_t es = elem_size(c->cfg.dtype);
-    const cuuint64_t d = c->cfg.head_dim;
-    cuuint64_t dims[3] = {d, static_cast<cuuint64_t>(p->page_size),
+    const cuuint64_t es = elem_size(c->cfg.dtype), d = c->cfg.head_dim, cols = 128 / es;
+    cuuint64_t dims[4] = {cols, static_cast<cuuint64_t>(p->page_size), d / cols,
                           static_cast<cuuint64_t>(p->slots) * p->num_pages * c->cfg.num_kv_heads};
-    cuuint64_t strides[2] = {d * es, d * es * p->page_size};
-    cuuint32_t box[3] = {static_cast<cuuint32_t>(decode_paged_box_cols(f32)), static_cast<cuuint32_t>(box_rows), 1u};
-    cuuint32_t estr[3] = {1u, 1u, 1u};
-    return fn(out, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+    cuuint64_t strides[3] = {d * es, 128, d * es * p->page_size};
+    cuuint32_t box[4] = {static_cast<cuuint32_t>(cols), static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(d / cols), 1u};
+    cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    return fn(out, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
               const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

@@ -27,7 +27,17 @@
 
 namespace kvs {
 
-constexpr int PAGED_SMEM_MAX = 232448 - 7168;   // dynamic share of an SM's 227 KB (static beside it)
+constexpr int PAGED_SMEM_MAX = 232448 - 3072;   // dynamic share of an SM's 227 KB (static beside it)
+
+// 4-D tiled bulk tensor load global -> shared, completion counted on `bar`.
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                            uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+        : "memory");
+}
 
 // Zero rows [r0, r1) of a staged tile: `subs` blocks of `sub_stride` bytes, 128 bytes a row.
 __device__ __forceinline__ void zero_rows(uint8_t* base, int subs, int sub_stride, int r0, int r1, int lane) {
@@ -39,6 +49,18 @@ __device__ __forceinline__ void zero_rows(uint8_t* base, int subs, int sub_strid
 
 // 1 / l; 0 where no token was attended to
 __device__ __forceinline__ float inverse_of(float l) { return l > 0.f ? 1.f / l : 0.f; }
+
+// Add a state's values v (x, z of one head with statistics mx, y, w of another with my) against
+// the joint maxima M.
+__device__ __forceinline__ void add_state(float4& acc, float2& l, const float4& v, float2 mx, float2 my, float2 M) {
+    const float fx = merge_factor(mx.x, M.x), fy = merge_factor(my.x, M.y);
+    l.x = fmaf(fx, mx.y, l.x);
+    l.y = fmaf(fy, my.y, l.y);
+    acc.x = fmaf(fx, v.x, acc.x);
+    acc.y = fmaf(fy, v.y, acc.y);
+    acc.z = fmaf(fx, v.z, acc.z);
+    acc.w = fmaf(fy, v.w, acc.w);
+}
 
 // P: the arithmetic of one storage type (see PagedBf16, PagedF32). It fixes D, NSRC, TT, NH
 // (padded heads), NW (warps), NSW (stages), SUBW (elements of a 128-byte row), STAGE (bytes)
@@ -72,14 +94,13 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     constexpr int D = P::D, TT = P::TT, NW = P::NW, NSW = P::NSW, NH = P::NH;
     constexpr int BLK = TT / 16;                 // 16-token blocks of a tile, each with its own limit
     constexpr int SUBS = D / P::SUBW;            // 128-byte wide sub-tiles of a tile
-    constexpr int SUB_BYTES = TT * 128;
-    constexpr int TILE_BYTES = SUBS * SUB_BYTES;
+    constexpr int TILE_BYTES = SUBS * TT * 128;
     extern __shared__ uint8_t smem_dyn[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
     __shared__ __align__(8) uint64_t bars[NW * NSW];
     __shared__ int s_lim[NW * NSW * BLK];
     __shared__ PagedState s_state[NW * 2];
-    __shared__ float s_m[NW * 2][NH], s_l[NW * 2][NH];
+    __shared__ float2 s_ml[NW * 2][NH];          // max and sum of every head of a state
     __shared__ int s_part[2][3];                 // units that continue elsewhere: first head, first CTA, CTAs
     __shared__ unsigned s_last[2];
 
@@ -177,6 +198,9 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     uint64_t* wb = &bars[warp * NSW];
     int* lims = &s_lim[warp * NSW * BLK];
     const int rows = min(ps, TT);                // tokens of one copy
+    // a copy lands as [sub-tile][rows][128 bytes]: strides of 16-token blocks and of sub-tiles
+    const int blk_stride = BLK == 1 || rows == TT ? 16 * 128 : SUBS * 16 * 128;
+    const int sub_stride = BLK == 1 ? TT * 128 : rows * 128;
     Cursor ic = at;
     int wbase = 0;                               // window: lane i holds the unit's (wbase + i)-th block
     int wphys = -1, wlog = -1;
@@ -201,15 +225,6 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         }
         wvalid = true;
     };
-    // one lane per copy: piece of the tile, sub-tile, K or V, source
-    constexpr int PB = SUBS * 2 * P::NSRC;       // copies of one page piece
-    static_assert(PB * (TT > 16 ? 2 : 1) <= 32, "one lane per copy");
-    const int pc_r = (lane / PB) * rows;         // this lane's piece starts at token pc_r of a tile
-    const int pc_h = lane % SUBS;
-    const int pc_side = (lane % PB) / SUBS;      // K, V (, K, V of the second source)
-    const CUtensorMap* pc_map = (pc_side & 1) ? &tmV : &tmK;
-    const int pc_slot = ((pc_side >> 1) ? a.src1 : a.src0) * a.num_pages;
-    const int pc_off = pc_side * TILE_BYTES + pc_h * SUB_BYTES + pc_r * 128;
     auto issue = [&](int k) {
         if (ic.t == ic.tiles) {
             next_unit(ic);
@@ -219,15 +234,26 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         const int blk = tok >> a.page_shift;
         if (!wvalid || blk >= wbase + 32) load_window(blk);
         const int s = k % NSW;
-        // lane i looks up the piece it copies; lanes below BLK also the limit of block i
-        const int phys = __shfl_sync(0xffffffffu, wphys, (((tok + pc_r) >> a.page_shift) - wbase) & 31);
-        const int lim_tok = tok + (lane % BLK) * 16;
-        const int lg = __shfl_sync(0xffffffffu, wlog, (lim_tok >> a.page_shift) - wbase);
-        if (lane < BLK) lims[s * BLK + lane] = lg < 0 ? 0 : ic.n - (lg << a.page_shift) - (lim_tok & (ps - 1));
+        // lane i looks up 16-token block i of the tile: its page, row and limit
+        const int my_tok = tok + (lane % BLK) * 16;
+        const int from = (my_tok >> a.page_shift) - wbase;
+        const int lg = __shfl_sync(0xffffffffu, wlog, from);
+        const int phys = __shfl_sync(0xffffffffu, wphys, from);
+        const int in_page = my_tok & (ps - 1);
+        if (lane < BLK) lims[s * BLK + lane] = lg < 0 ? 0 : ic.n - (lg << a.page_shift) - in_page;
         if (lane == 0) mbar_arrive_expect_tx(&wb[s], P::STAGE);
-        if (pc_r < TT)
-            tma_load_3d(ring + s * P::STAGE + pc_off, pc_map, pc_h * P::SUBW, (tok + pc_r) & (ps - 1),
-                        phys < 0 ? -1 : (pc_slot + phys) * a.Hkv + ic.j, &wb[s]);
+        // the first lane of a page piece copies it
+        if (lane < BLK && (lane * 16) % rows == 0) {
+            uint8_t* dst = ring + s * P::STAGE + lane * blk_stride;
+            const int c0 = phys < 0 ? -1 : (a.src0 * a.num_pages + phys) * a.Hkv + ic.j;
+            tma_load_4d(dst, &tmK, 0, in_page, 0, c0, &wb[s]);
+            tma_load_4d(dst + TILE_BYTES, &tmV, 0, in_page, 0, c0, &wb[s]);
+            if (P::NSRC == 2) {
+                const int c1 = phys < 0 ? -1 : (a.src1 * a.num_pages + phys) * a.Hkv + ic.j;
+                tma_load_4d(dst + 2 * TILE_BYTES, &tmK, 0, in_page, 0, c1, &wb[s]);
+                tma_load_4d(dst + 3 * TILE_BYTES, &tmV, 0, in_page, 0, c1, &wb[s]);
+            }
+        }
         ++ic.t;
         __syncwarp();
     };
@@ -243,7 +269,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 
     // ---- stream the share
     P p;
-    float* save = reinterpret_cast<float*>(smem + L::RING) + warp * NH * D;
+    float4* save = reinterpret_cast<float4*>(smem + L::RING) + warp * P::VALS;
     p.setup(reinterpret_cast<float*>(smem + L::RING + L::SAVE) + warp * P::WARP_FLOATS, lane);
     Cursor cc = at;
     int first_tile = at.t;                       // first tile of the current unit in this share
@@ -253,24 +279,25 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         const bool started = first_tile == 0, ended = cc.t == cc.tiles;
         const int head0 = cc.b * a.Hq + cc.j * g;
         if (started && ended) {
-            p.each(g, [&](int h, int e, float v, float inv) { a.out[static_cast<size_t>(head0 + h) * D + e] = v * inv; });
+            p.values([&](int i, const float4& v) {
+                const float2 l = p.sums(i);
+                P::emit(a.out + static_cast<size_t>(head0) * D, g, i, v, make_float2(inverse_of(l.x), inverse_of(l.y)));
+            });
             if (a.lse != nullptr) p.stats(g, [&](int h, float m, float l) { a.lse[head0 + h] = lse_of(m, l); });
             return;
         }
         const int which = 2 * warp + (started ? 1 : 0);
-        float* dst = started ? reinterpret_cast<float*>(ring) : save;
-        p.each(g, [&](int h, int e, float v, float) { dst[h * D + e] = v; });
-        p.stats(g, [&](int h, float m, float l) {
-            s_m[which][h] = m;
-            s_l[which][h] = l;
-        });
+        float4* dst = started ? reinterpret_cast<float4*>(ring) : save;
+        p.values([&](int i, const float4& v) { dst[i] = v; });
+        p.stats(g, [&](int h, float m, float l) { s_ml[which][h] = make_float2(m, l); });
         if (lane == 0)
             s_state[which] = {head0, static_cast<int>(t0) + k - cc.t, cc.tiles, started ? 1 : 0, ended ? 1 : 0};
     };
     if (my_n > 0) p.begin(a, cc.b, cc.j);
-    for (int k = 0; k < my_n; ++k) {
-        if (cc.t == cc.tiles) {
+    for (int k = 0; my_n > 0; ++k) {
+        if (k == my_n || cc.t == cc.tiles) {
             end_unit(k);
+            if (k == my_n) break;
             next_unit(cc);
             first_tile = 0;
             p.begin(a, cc.b, cc.j);
@@ -290,18 +317,17 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 const int lim = lims[s * BLK + i];
                 if (lim >= 16) continue;
                 cut = true;
-                zero_rows(st + TILE_BYTES, SUBS, SUB_BYTES, i * 16 + max(lim, 0), i * 16 + 16, lane);
-                if (P::NSRC == 2) zero_rows(st + 3 * TILE_BYTES, SUBS, SUB_BYTES, i * 16 + max(lim, 0), i * 16 + 16, lane);
+                zero_rows(st + TILE_BYTES + i * blk_stride, SUBS, sub_stride, max(lim, 0), 16, lane);
+                if (P::NSRC == 2) zero_rows(st + 3 * TILE_BYTES + i * blk_stride, SUBS, sub_stride, max(lim, 0), 16, lane);
             }
             if (cut) __syncwarp();
-            p.tile(a, st, lims + s * BLK, cut);
+            p.tile(a, st, blk_stride, sub_stride, lims + s * BLK, cut);
             if (cut) fence_proxy_async();        // the cleared rows before the next copy into the stage
             __syncwarp();
             if (k + NSW < my_n) issue(k + NSW);
         }
         ++cc.t;
     }
-    if (my_n > 0) end_unit(my_n);
     __syncthreads();
 
     // ---- join the warps' states, unit by unit. States are in the line's order; every warp
@@ -336,43 +362,60 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         part[1] = owner(mine.begin);
         part[2] = owner(mine.begin + mine.tiles - 1) - part[1] + 1;
     }
-    const int per = paged_partial(g, D);
-    const int items = g * (D / 4), groups = __popc(firsts);
-    for (int k = threadIdx.x; k < groups * items; k += NW * 32) {
-        const int idx = k % items;
+    constexpr int per = paged_partial(NH, D), VALS = P::VALS;
+    static_assert(VALS * 4 == NH * D, "a state's values");
+    const int groups = __popc(firsts);
+    for (int k = threadIdx.x; k < groups * VALS; k += NW * 32) {
+        const int idx = k % VALS;
+        const int2 hd = P::heads(idx);
+        if (hd.x >= g) continue;
         unsigned rest = firsts;
-        for (int c = k / items; c > 0; --c) rest &= rest - 1u;
+        for (int c = k / VALS; c > 0; --c) rest &= rest - 1u;
         const int i = __ffs(rest) - 1;
         const unsigned states = states_from(i);
-        const int h = idx / (D / 4), e = (idx % (D / 4)) * 4;
-        float M = NEG_INF;
-#pragma unroll
-        for (int s = 0; s < 2 * NW; ++s)
-            if ((states >> s) & 1u) M = fmaxf(M, s_m[s][h]);
+        // two states at a time, their loads together (a missing second one is the first, weight 0)
+        float2 M = make_float2(NEG_INF, NEG_INF);
+        for (unsigned r = states; r != 0u;) {
+            const int s0 = __ffs(r) - 1;
+            r &= r - 1u;
+            const int s1 = r ? __ffs(r) - 1 : s0;
+            r &= r - 1u;
+            M.x = fmaxf(M.x, fmaxf(s_ml[s0][hd.x].x, s_ml[s1][hd.x].x));
+            M.y = fmaxf(M.y, fmaxf(s_ml[s0][hd.y].x, s_ml[s1][hd.y].x));
+        }
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l = 0.f;
-#pragma unroll
-        for (int s = 0; s < 2 * NW; ++s) {
-            if (!((states >> s) & 1u)) continue;
-            const float f = merge_factor(s_m[s][h], M);
-            // odd states lie over their warp's ring, even ones in the save area
-            const float4 v = *reinterpret_cast<const float4*>(
-                smem + ((s & 1) ? (s >> 1) * NSW * P::STAGE : L::RING + (s >> 1) * NH * D * 4) + (h * D + e) * 4);
-            l = fmaf(f, s_l[s][h], l);
-            acc.x = fmaf(f, v.x, acc.x);
-            acc.y = fmaf(f, v.y, acc.y);
-            acc.z = fmaf(f, v.z, acc.z);
-            acc.w = fmaf(f, v.w, acc.w);
+        float2 l = make_float2(0.f, 0.f);
+        // odd states lie over their warp's ring, even ones in the save area
+        auto value = [&](int s) {
+            return reinterpret_cast<const float4*>(smem + ((s & 1) ? (s >> 1) * NSW * P::STAGE : L::RING + (s >> 1) * VALS * 16))[idx];
+        };
+        for (unsigned r = states; r != 0u;) {
+            const int s0 = __ffs(r) - 1;
+            r &= r - 1u;
+            const bool two = r != 0u;
+            const int s1 = two ? __ffs(r) - 1 : s0;
+            r &= r - 1u;
+            const float4 v0 = value(s0), v1 = value(s1);
+            const float2 x0 = s_ml[s0][hd.x], y0 = s_ml[s0][hd.y], x1 = s_ml[s1][hd.x], y1 = s_ml[s1][hd.y];
+            add_state(acc, l, v0, x0, y0, M);
+            if (two) add_state(acc, l, v1, x1, y1, M);
         }
         if ((splits >> i) & 1u) {
             float* part = a.ws + static_cast<size_t>(2 * cta + s_state[i].started) * per;
-            *reinterpret_cast<float4*>(part + h * D + e) = acc;
-            if (e == 0) *reinterpret_cast<float2*>(part + g * D + 2 * h) = make_float2(M, l);
+            reinterpret_cast<float4*>(part)[idx] = acc;
+            // the lanes that hold a head's first channels write its statistics
+            if (P::first_of(idx)) {
+                float2* ml = reinterpret_cast<float2*>(part + NH * D);
+                ml[hd.x] = make_float2(M.x, l.x);
+                ml[hd.y] = make_float2(M.y, l.y);
+            }
         } else {
-            const int head = s_state[i].head0 + h;
-            const float inv = inverse_of(l);
-            *reinterpret_cast<float4*>(a.out + static_cast<size_t>(head) * D + e) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-            if (e == 0 && a.lse != nullptr) a.lse[head] = lse_of(M, l);
+            const int head0 = s_state[i].head0;
+            P::emit(a.out + static_cast<size_t>(head0) * D, g, idx, acc, make_float2(inverse_of(l.x), inverse_of(l.y)));
+            if (a.lse != nullptr && P::first_of(idx)) {
+                a.lse[head0 + hd.x] = lse_of(M.x, l.x);
+                if (hd.y < g) a.lse[head0 + hd.y] = lse_of(M.y, l.y);
+            }
         }
     }
     if (splits == 0u) return;
@@ -389,7 +432,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         s_last[threadIdx.x] = prev_n == static_cast<unsigned>(s_part[threadIdx.x][2] - 1) ? 1u : 0u;
     }
     __syncthreads();
-    float2* stat = reinterpret_cast<float2*>(smem);      // [n][g] (m, l), over the ring
+    float2* stat = reinterpret_cast<float2*>(smem);      // [n][NH] (m, l), over the ring
     for (int which = 0; which < 2; ++which) {
         const int head0 = s_part[which][0];
         if (head0 < 0 || s_last[which] == 0u) continue;  // the same for every thread
@@ -399,43 +442,38 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         auto slot = [&](int i) { return base + (2 * i + (i == 0 ? 1 : 0)) * per; };
         // a thread's first values are on their way while the statistics are shared
         constexpr int AHEAD = 4;
-        const int h0 = threadIdx.x / (D / 4), e0 = (threadIdx.x % (D / 4)) * 4;
-        float4 v0[AHEAD];
-        if (threadIdx.x < items) {
+        float4 early[AHEAD];
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i)
-                if (i < n) v0[i] = __ldcg(reinterpret_cast<const float4*>(slot(i) + h0 * D + e0));
-        }
-        for (int i = warp; i < n; i += NW)
-            if (lane < g) stat[i * g + lane] = __ldcg(reinterpret_cast<const float2*>(slot(i) + g * D) + lane);
+        for (int i = 0; i < AHEAD; ++i)
+            if (i < n && threadIdx.x < VALS) early[i] = __ldcg(reinterpret_cast<const float4*>(slot(i)) + threadIdx.x);
+        for (int i = threadIdx.x; i < n * NH; i += NW * 32)
+            stat[i] = __ldcg(reinterpret_cast<const float2*>(slot(i / NH) + NH * D) + i % NH);
         __syncthreads();
-        for (int idx = threadIdx.x; idx < items; idx += NW * 32) {
-            const int h = idx / (D / 4), e = (idx % (D / 4)) * 4;
-            float M = NEG_INF;
+        for (int idx = threadIdx.x; idx < VALS; idx += NW * 32) {
+            const int2 hd = P::heads(idx);
+            if (hd.x >= g) continue;
+            float2 M = make_float2(NEG_INF, NEG_INF);
 #pragma unroll 4
-            for (int i = 0; i < n; ++i) M = fmaxf(M, stat[i * g + h].x);
+            for (int i = 0; i < n; ++i) {
+                M.x = fmaxf(M.x, stat[i * NH + hd.x].x);
+                M.y = fmaxf(M.y, stat[i * NH + hd.y].x);
+            }
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            float l = 0.f;
-            auto add = [&](int i, const float4& v) {
-                const float2 ml = stat[i * g + h];
-                const float f = merge_factor(ml.x, M);
-                l = fmaf(f, ml.y, l);
-                acc.x = fmaf(f, v.x, acc.x);
-                acc.y = fmaf(f, v.y, acc.y);
-                acc.z = fmaf(f, v.z, acc.z);
-                acc.w = fmaf(f, v.w, acc.w);
-            };
+            float2 l = make_float2(0.f, 0.f);
             int i = 0;
             if (idx == threadIdx.x) {
 #pragma unroll
                 for (; i < AHEAD; ++i)
-                    if (i < n) add(i, v0[i]);
+                    if (i < n) add_state(acc, l, early[i], stat[i * NH + hd.x], stat[i * NH + hd.y], M);
             }
 #pragma unroll 4
-            for (; i < n; ++i) add(i, __ldcg(reinterpret_cast<const float4*>(slot(i) + h * D + e)));
-            const float inv = inverse_of(l);
-            *reinterpret_cast<float4*>(a.out + static_cast<size_t>(head0 + h) * D + e) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-            if (e == 0 && a.lse != nullptr) a.lse[head0 + h] = lse_of(M, l);
+            for (; i < n; ++i)
+                add_state(acc, l, __ldcg(reinterpret_cast<const float4*>(slot(i)) + idx), stat[i * NH + hd.x], stat[i * NH + hd.y], M);
+            P::emit(a.out + static_cast<size_t>(head0) * D, g, idx, acc, make_float2(inverse_of(l.x), inverse_of(l.y)));
+            if (a.lse != nullptr && P::first_of(idx)) {
+                a.lse[head0 + hd.x] = lse_of(M.x, l.x);
+                if (hd.y < g) a.lse[head0 + hd.y] = lse_of(M.y, l.y);
+            }
         }
         if (threadIdx.x == 0) a.counters[c0] = 0u;
         __syncthreads();

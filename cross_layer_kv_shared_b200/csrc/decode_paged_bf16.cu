@@ -18,13 +18,13 @@ namespace {
 template <int D_, bool MIX, int NH_>
 struct PagedBf16 {
     static constexpr int D = D_, NH = NH_, NSRC = MIX ? 2 : 1;
-    static constexpr int TT = (MIX && D == 128) ? 16 : 32;
+    static constexpr int TT = D == 128 ? 16 : 32;
     static constexpr int SUBW = 64;
     static constexpr int STAGE = 2 * NSRC * TT * D * 2;
     static constexpr int NW = STAGE <= 8192 ? 8 : 4;
     static constexpr int WARP_FLOATS = 0;
     static constexpr int NSW = paged_stages(NW, STAGE, NH, D, WARP_FLOATS);
-    static constexpr int MT = TT / 16, NB = NH / 8, SUB_BYTES = TT * 128, TILE_BYTES = TT * D * 2;
+    static constexpr int MT = TT / 16, NB = NH / 8, TILE_BYTES = TT * D * 2;
 
     uint32_t qb[D / 16][NB][2];      // B fragments of Q^T: column n = head nb*8 + lane/4
     float o[D / 16][NB][4];          // O^T: rows = channels, columns = heads nb*8 + 2(lane%4) (+1)
@@ -62,7 +62,7 @@ struct PagedBf16 {
         return movmatrix_t(x);
     }
 
-    __device__ void tile(const PagedDecodeArgs& a, const uint8_t* st, const int* lim, bool cut) {
+    __device__ void tile(const PagedDecodeArgs& a, const uint8_t* st, int blk_stride, int sub_stride, const int* lim, bool cut) {
         const uint32_t kb = smem_u32(st), vb = kb + TILE_BYTES;
         const int mi = lane >> 3, ri = lane & 7;     // ldmatrix: matrix and row this lane addresses
         float sc[MT][NB][4];
@@ -73,11 +73,11 @@ struct PagedBf16 {
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sc[mt][nb][i] = s2[nb][i] = 0.f;
-            const int row = mt * 16 + (mi & 1) * 8 + ri;
+            const int row = (mi & 1) * 8 + ri;
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
                 const int c = ks * 2 + (mi >> 1);
-                const uint32_t off = (c >> 3) * SUB_BYTES + swz128(row, c & 7);
+                const uint32_t off = mt * blk_stride + (c >> 3) * sub_stride + swz128(row, c & 7);
                 uint32_t af[4];
                 ldsm_x4(kb + off, af[0], af[1], af[2], af[3]);
 #pragma unroll
@@ -155,9 +155,9 @@ struct PagedBf16 {
             for (int nb = 0; nb < NB; ++nb) acc[nb][0] = acc[nb][1] = acc[nb][2] = acc[nb][3] = 0.f;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                const int row = mt * 16 + (mi >> 1) * 8 + ri;
+                const int row = (mi >> 1) * 8 + ri;
                 const int c = dt * 2 + (mi & 1);
-                const uint32_t off = (c >> 3) * SUB_BYTES + swz128(row, c & 7);
+                const uint32_t off = mt * blk_stride + (c >> 3) * sub_stride + swz128(row, c & 7);
 #pragma unroll
                 for (int src = 0; src < NSRC; ++src) {
                     uint32_t af[4];
@@ -186,20 +186,38 @@ struct PagedBf16 {
             }
     }
 
-    // f(head, channel, value, 1 / l) for what this lane holds of the unit
+    // A state's values as float4s in this order, so that saving and joining are 16-byte moves:
+    // value (dt, nb) of lane i holds channels e, e + 8 of heads h, h + 1
+    static constexpr int VALS = NB * (D / 16) * 32;
     template <typename F>
-    __device__ void each(int g, F f) {
+    __device__ void values(F f) const {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            const float inv[2] = {inverse_of(l[nb][0]), inverse_of(l[nb][1])};
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int dt = 0; dt < D / 16; ++dt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int h = nb * 8 + 2 * (lane & 3) + (i & 1);
-                    if (h < g) f(h, dt * 16 + (lane >> 2) + (i >> 1) * 8, o[dt][nb][i], inv[i & 1]);
-                }
+                f((nb * (D / 16) + dt) * 32 + lane, make_float4(o[dt][nb][0], o[dt][nb][1], o[dt][nb][2], o[dt][nb][3]));
+    }
+    // the heads of value k: x and z belong to .x, y and w to .y
+    __device__ static int2 heads(int k) {
+        const int h = k / (32 * (D / 16)) * 8 + 2 * (k & 3);
+        return make_int2(h, h + 1);
+    }
+    __device__ static bool first_of(int k) { return k % (32 * (D / 16)) < 4; }    // channel 0
+    __device__ static void emit(float* out, int g, int k, const float4& v, float2 inv) {
+        const int h = heads(k).x, e = (k / 32) % (D / 16) * 16 + (k & 31) / 4;
+        float* at = out + h * D + e;
+        if (h < g) {
+            at[0] = v.x * inv.x;
+            at[8] = v.z * inv.x;
         }
+        if (h + 1 < g) {
+            at[D] = v.y * inv.y;
+            at[D + 8] = v.w * inv.y;
+        }
+    }
+    __device__ float2 sums(int k) const {
+        const int nb = k / (32 * (D / 16));
+        return make_float2(l[nb][0], l[nb][1]);
     }
 
     template <typename F>
@@ -224,8 +242,9 @@ cudaError_t launch_g(const CUtensorMap& tmK, const CUtensorMap& tmV, const Paged
 }  // namespace
 
 int decode_paged_box_rows(bool f32, int d, bool mix, int page_size) {
-    const int tt = f32 || (mix && d == 128) ? 16 : 32;
-    static_assert(PagedBf16<128, true, 8>::TT == 16 && PagedBf16<128, false, 8>::TT == 32 &&
+    (void)mix;
+    const int tt = f32 || d == 128 ? 16 : 32;
+    static_assert(PagedBf16<128, true, 8>::TT == 16 && PagedBf16<128, false, 8>::TT == 16 &&
                       PagedBf16<64, true, 8>::TT == 32 && PagedBf16<64, false, 8>::TT == 32,
                   "tile rows");
     return page_size < tt ? page_size : tt;

@@ -80,7 +80,7 @@ struct PagedF32 {
         }
     }
 
-    __device__ void tile(const PagedDecodeArgs& a, const uint8_t* st, const int* lim, bool cut) {
+    __device__ void tile(const PagedDecodeArgs& a, const uint8_t* st, int, int, const int* lim, bool cut) {
         const int quarter = lane >> 3;
         float acc[2][NH];
 #pragma unroll
@@ -191,22 +191,24 @@ struct PagedF32 {
         __syncwarp();
         if ((lane & 7) == 0)
 #pragma unroll
-            for (int h = 0; h < HQ; ++h) sc[(lane >> 3) * HQ + h] = inverse_of(l[h]);
+            for (int h = 0; h < HQ; ++h) sc[(lane >> 3) * HQ + h] = l[h];
         __syncwarp();
     }
 
-    // f(head, channel, value, 1 / l) for what this lane holds of the unit
+    // a state's values as float4s: head k / EL, channels 4 (k % EL) ..
+    static constexpr int VALS = NH * EL;
     template <typename F>
-    __device__ void each(int g, F f) {
+    __device__ void values(F f) const {
         if (lane >= EL) return;
 #pragma unroll
-        for (int h = 0; h < NH; ++h)
-            if (h < g) {
-                const float inv = sc[h];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) f(h, lane * 4 + x, o[h][x], inv);
-            }
+        for (int h = 0; h < NH; ++h) f(h * EL + lane, make_float4(o[h][0], o[h][1], o[h][2], o[h][3]));
     }
+    __device__ static int2 heads(int k) { return make_int2(k / EL, k / EL); }
+    __device__ static bool first_of(int k) { return k % EL == 0; }    // channel 0
+    __device__ static void emit(float* out, int g, int k, const float4& v, float2 inv) {
+        if (k / EL < g) *reinterpret_cast<float4*>(out + 4 * k) = make_float4(v.x * inv.x, v.y * inv.x, v.z * inv.x, v.w * inv.x);
+    }
+    __device__ float2 sums(int k) const { return make_float2(sc[k / EL], sc[k / EL]); }
 
     template <typename F>
     __device__ void stats(int g, F f) {

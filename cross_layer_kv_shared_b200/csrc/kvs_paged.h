@@ -27,23 +27,22 @@ struct PagedDecodeArgs {
     int B, Hq, Hkv, g;
     int num_pages, max_blocks, page_shift, top;
     float scale_log2;       // softmax scale * log2(e)
-    float* ws;              // split partials: two slots per CTA, each [g][d] o, [g] m, [g] l
+    float* ws;              // split partials: two slots per CTA (paged_partial floats each)
     unsigned* counters;     // [CTAs] arrival counters, zero between launches
     unsigned* err;
     long long wait_limit;
     int ctas;               // grid: at most one CTA per SM
 };
-// rows of the K/V tensor-map boxes (tokens per copy) and their width in elements
+// rows of the K/V tensor-map boxes (tokens per copy)
 int decode_paged_box_rows(bool f32, int d, bool mix, int page_size);
-inline int decode_paged_box_cols(bool f32) { return f32 ? 32 : 64; }
 cudaError_t launch_decode_paged_bf16(int d, bool mix, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                      const PagedDecodeArgs& a, cudaStream_t st);
 cudaError_t launch_decode_paged_f32(int d, bool mix, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                     const PagedDecodeArgs& a, cudaStream_t st);
-// floats of one partial ([g][d] o, [g] m, [g] l), padded so that every slot is 16-byte aligned
-__host__ __device__ constexpr int paged_partial(int g, int d) { return g * d + ((2 * g + 3) & ~3); }
+// floats of one partial: nh (padded) heads' o, then their (m, l) pairs; slots stay 16-byte aligned
+__host__ __device__ constexpr int paged_partial(int nh, int d) { return nh * (d + 2); }
 // floats one CTA may need in PagedDecodeArgs::ws
-inline size_t paged_ws_floats(int g, int d) { return 2 * static_cast<size_t>(paged_partial(g, d)); }
+inline size_t paged_ws_floats(int g, int d) { return 2 * static_cast<size_t>(paged_partial(g <= 8 ? 8 : 16, d)); }
 
 // Block selection of one layer.
 struct PagedSelectArgs {
