@@ -29,14 +29,20 @@ namespace kvs {
 
 constexpr int PAGED_SMEM_MAX = 232448 - 3072;   // dynamic share of an SM's 227 KB (static beside it)
 
-// 4-D tiled bulk tensor load global -> shared, completion counted on `bar`.
+// 4-D tiled bulk tensor load global -> shared with an L2 policy, completion counted on `bar`.
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
-                                            uint64_t* bar) {
+                                            uint64_t* bar, uint64_t policy) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar)), "l"(policy)
         : "memory");
+}
+
+__device__ __forceinline__ uint64_t policy_evict_first() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
 }
 
 // Zero rows [r0, r1) of a staged tile: `subs` blocks of `sub_stride` bytes, 128 bytes a row.
@@ -225,6 +231,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         }
         wvalid = true;
     };
+    const uint64_t policy = policy_evict_first();
     auto issue = [&](int k) {
         if (ic.t == ic.tiles) {
             next_unit(ic);
@@ -246,12 +253,12 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         if (lane < BLK && (lane * 16) % rows == 0) {
             uint8_t* dst = ring + s * P::STAGE + lane * blk_stride;
             const int c0 = phys < 0 ? -1 : (a.src0 * a.num_pages + phys) * a.Hkv + ic.j;
-            tma_load_4d(dst, &tmK, 0, in_page, 0, c0, &wb[s]);
-            tma_load_4d(dst + TILE_BYTES, &tmV, 0, in_page, 0, c0, &wb[s]);
+            tma_load_4d(dst, &tmK, 0, in_page, 0, c0, &wb[s], policy);
+            tma_load_4d(dst + TILE_BYTES, &tmV, 0, in_page, 0, c0, &wb[s], policy);
             if (P::NSRC == 2) {
                 const int c1 = phys < 0 ? -1 : (a.src1 * a.num_pages + phys) * a.Hkv + ic.j;
-                tma_load_4d(dst + 2 * TILE_BYTES, &tmK, 0, in_page, 0, c1, &wb[s]);
-                tma_load_4d(dst + 3 * TILE_BYTES, &tmV, 0, in_page, 0, c1, &wb[s]);
+                tma_load_4d(dst + 2 * TILE_BYTES, &tmK, 0, in_page, 0, c1, &wb[s], policy);
+                tma_load_4d(dst + 3 * TILE_BYTES, &tmV, 0, in_page, 0, c1, &wb[s], policy);
             }
         }
         ++ic.t;
