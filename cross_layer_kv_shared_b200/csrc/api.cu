@@ -442,8 +442,7 @@ kvshare_status kvshare_create(const kvshare_config* cfg, kvshare_t* out) {
         cudaMalloc(&ctx->err, sizeof(unsigned)) != cudaSuccess ||
         cudaMalloc(&ctx->w_dev, ctx->w_host.size() * sizeof(float)) != cudaSuccess ||
         cudaMalloc(&ctx->pg_ws, paged_ws_floats(g, c.head_dim) * ctx->sms * sizeof(float)) != cudaSuccess ||
-        cudaMalloc(&ctx->pg_counters, (ctx->sms + 1) * sizeof(unsigned)) != cudaSuccess ||
-        cudaMalloc(&ctx->pg_score, units * ((c.max_context + 15) / 16) * sizeof(float)) != cudaSuccess) {
+        cudaMalloc(&ctx->pg_counters, (ctx->sms + 1) * sizeof(unsigned)) != cudaSuccess) {
         cudaGetLastError();
         kvshare_destroy(ctx);
         return KVS_ENOMEM;
@@ -471,7 +470,6 @@ kvshare_status kvshare_destroy(kvshare_t ctx) {
     cudaFree(ctx->w_dev);
     cudaFree(ctx->pg_ws);
     cudaFree(ctx->pg_counters);
-    cudaFree(ctx->pg_score);
     cudaFree(ctx->sscore);
     cudaFree(ctx->qp);
     cudaFree(ctx->q_stage);

@@ -253,8 +253,7 @@ kvshare_status kvshare_select_pages(kvshare_t ctx, const kvshare_pages* pages, c
     if (s == KVS_OK) s = check_layers(ctx, pages, l0, l1);
     if (s != KVS_OK) return s;
     if (first < 0 || last < 1 || top < 1 || first > top || last > top - first) return KVS_EINVAL;
-    if (pages->max_blocks > SELECT_MAX_BLOCKS || pages->batch > 65535 || ctx->cfg.num_kv_heads > 65535)
-        return KVS_EUNSUPPORTED;
+    if (pages->max_blocks > SELECT_MAX_BLOCKS) return KVS_EUNSUPPORTED;
     if (!on_device(ctx, q, 16) || !on_device(ctx, selected, 4) || !on_device(ctx, pages->bound_codes, 16) ||
         !on_device(ctx, pages->bound_scale, 4))
         return KVS_EINVAL;
@@ -273,7 +272,6 @@ kvshare_status kvshare_select_pages(kvshare_t ctx, const kvshare_pages* pages, c
         a.table = pages->block_table;
         a.lens = pages->lengths;
         a.w = ctx->w_dev + static_cast<size_t>(l) * Hkv;
-        a.score = ctx->pg_score;
         a.sel = selected + static_cast<size_t>(l) * B * Hkv * top;
         a.mix = e.kind == KVS_SRC_MIX;
         a.src0 = e.src0;
@@ -291,9 +289,8 @@ kvshare_status kvshare_select_pages(kvshare_t ctx, const kvshare_pages* pages, c
         a.last = last;
         a.f32 = cf.dtype == KVS_F32;
         a.err = ctx->err;
-        const int n = launch_select_pages(a, static_cast<cudaStream_t>(stream));
-        if (n < 0) return KVS_ECUDA;
-        ctx->launches += n;
+        if (launch_select_pages(a, ctx->sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) return KVS_ECUDA;
+        ++ctx->launches;
     }
     return KVS_OK;
 }

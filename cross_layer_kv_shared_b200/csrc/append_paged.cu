@@ -24,8 +24,8 @@ constexpr int NT = 256;
 constexpr int UNROLL = 8;
 
 struct Grid {
-    int copy_blocks, copy_tokens;     // copy blocks and the tokens of each
-    int bound_tokens;                 // tokens of a bound block
+    int bound_blocks, bound_tokens;   // bound blocks (first in the grid: theirs is the longer chain) and the tokens of each
+    int copy_tokens;                  // tokens of a copy block
 };
 
 __device__ __forceinline__ bool slot_ok(const PagedAppendArgs& a, int slot) {
@@ -112,17 +112,18 @@ __device__ void bound_page(const PagedAppendArgs& a, int i, int slot, int j) {
         hi[e] = NEG_INF;
         lo[e] = -NEG_INF;
     }
-    for (int r = lane / P; r <= r1; r += ROWS * UNROLL) {
-        uint4 x[UNROLL];
+    constexpr int DEEP = 16;                            // rows of a lane in flight
+    for (int r = lane / P; r <= r1; r += ROWS * DEEP) {
+        uint4 x[DEEP];
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
+        for (int u = 0; u < DEEP; ++u) {
             const int row = min(r + u * ROWS, r1);      // the last row again changes nothing
             const char* at = row < old ? held + static_cast<size_t>(row) * RB
                                        : in + (static_cast<long long>(i - (r1 - row)) * a.k_stride) * ES;
             x[u] = *reinterpret_cast<const uint4*>(at);
         }
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u)
+        for (int u = 0; u < DEEP; ++u)
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const float v = elem<F32>(x[u], e);
@@ -171,13 +172,13 @@ template <bool F32, int RB>
 __global__ void __launch_bounds__(NT) append_paged_kernel(const PagedAppendArgs a, const Grid gr) {
     grid_dep_wait();
     if (threadIdx.x == 0) grid_dep_launch();
-    if (static_cast<int>(blockIdx.x) < gr.copy_blocks) {
-        copy_tokens<RB>(a, blockIdx.x * gr.copy_tokens, gr.copy_tokens);
+    if (static_cast<int>(blockIdx.x) >= gr.bound_blocks) {
+        copy_tokens<RB>(a, (blockIdx.x - gr.bound_blocks) * gr.copy_tokens, gr.copy_tokens);
         return;
     }
     // a page's last written row carries the page: the next token is elsewhere, or it is row page - 1
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int first = (blockIdx.x - gr.copy_blocks) * gr.bound_tokens;
+    const int first = blockIdx.x * gr.bound_tokens;
     const int i = first + lane;
     bool ends = false;
     if (lane < gr.bound_tokens && i < a.tokens) {
@@ -208,13 +209,14 @@ cudaError_t launch(const PagedAppendArgs& a, cudaStream_t st) {
     int tokens = side * UNROLL;
     while (tokens > side && (a.tokens + tokens - 1) / tokens < 296) tokens = (tokens / side + 1) / 2 * side;
     gr.copy_tokens = tokens;
-    gr.copy_blocks = (a.tokens + tokens - 1) / tokens;
-    int blocks = gr.copy_blocks;
+    int blocks = (a.tokens + tokens - 1) / tokens;
     gr.bound_tokens = 1;
+    gr.bound_blocks = 0;
     if (a.codes != nullptr) {
         const int bt = (a.tokens + 591) / 592;
-        gr.bound_tokens = bt < 1 ? 1 : bt > 32 ? 32 : bt;
-        blocks += (a.tokens + gr.bound_tokens - 1) / gr.bound_tokens;
+        gr.bound_tokens = bt > 32 ? 32 : bt;
+        gr.bound_blocks = (a.tokens + gr.bound_tokens - 1) / gr.bound_tokens;
+        blocks += gr.bound_blocks;
     }
     return launch_kernel(append_paged_kernel<F32, RB>, dim3(blocks), dim3(NT), 0, st, true, a, gr);
 }

@@ -22,6 +22,8 @@
 // pages (NaN included) reach no output.
 #pragma once
 
+#include <algorithm>
+
 #include "kvs_device.cuh"
 #include "kvs_paged.h"
 
@@ -145,26 +147,50 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     auto row_tiles = [&](int n) {
         return ((a.sel != nullptr ? row_blocks(n) << a.page_shift : n) + TT - 1) / TT;
     };
-    // 32-bit arithmetic: the caller keeps the line below 2^31 tiles
-    const int n_lane = lane < a.B ? row_len(lane) : 0;       // the first 32 sequences, one per lane
-    const int tiles_lane = row_tiles(n_lane);
-    unsigned total = tiles_lane;
-    for (int b = lane + 32; b < a.B; b += 32) total += row_tiles(row_len(b));
-    const unsigned W = __reduce_add_sync(0xffffffffu, total) * a.Hkv;
-    // no more CTAs than tiles: every CTA between a unit's first and last holds a part of it
-    const unsigned nc = max(1u, min(static_cast<unsigned>(a.ctas), (W + NW - 1) / NW));
-    const unsigned workers = nc * NW, share = W / workers, more = W - share * workers;
-    const unsigned id = cta * NW + warp;         // the first `more` warps take one tile more
-    const unsigned t0 = share * id + min(id, more);
-    const int my_n = id < workers ? share + (id < more ? 1 : 0) : 0;
-
     struct Cursor {
         int b, j, t, n, tiles;
     };
     Cursor at = {0, 0, 0, 0, 0};
-    if (my_n > 0) {
+    // entry i of a unit's block list and its page, unchecked (i within the list)
+    auto look_up = [&](int b, int j, int i, int& lg, int& ph) {
+        lg = i;
+        if (a.sel != nullptr) lg = a.sel[(static_cast<size_t>(b) * a.Hkv + j) * a.top + i];
+        ph = lg >= 0 && lg < a.max_blocks ? a.table[static_cast<size_t>(b) * a.max_blocks + lg] : -1;
+    };
+    const int list = a.sel != nullptr ? min(a.top, a.max_blocks) : a.max_blocks;   // longest block list
+    int early_lg = -1, early_ph = -1;
+    const bool early = a.aligned != 0 && list <= 32;         // the whole list, fetched beside the length
+    unsigned share, more, t0;
+    int my_n;
+    if (a.aligned) {
+        // one CTA per unit, its tiles dealt to the warps
+        at.b = cta / a.Hkv;
+        at.j = cta - at.b * a.Hkv;
+        if (early && lane < list) look_up(at.b, at.j, lane, early_lg, early_ph);
+        at.n = row_len(at.b);
+        at.tiles = row_tiles(at.n);
+        share = at.tiles / NW;
+        more = at.tiles - share * NW;
+        t0 = share * warp + min(static_cast<unsigned>(warp), more);
+        my_n = share + (warp < more ? 1 : 0);
+        at.t = t0;
+    } else {
+        // 32-bit arithmetic: the caller keeps the line below 2^31 tiles
+        const int n_lane = lane < a.B ? row_len(lane) : 0;   // the first 32 sequences, one per lane
+        const int tiles_lane = row_tiles(n_lane);
+        unsigned total = tiles_lane;
+        for (int b = lane + 32; b < a.B; b += 32) total += row_tiles(row_len(b));
+        const unsigned W = __reduce_add_sync(0xffffffffu, total) * a.Hkv;
+        // no more CTAs than tiles: every CTA between a unit's first and last holds a part of it
+        const unsigned nc = max(1u, min(static_cast<unsigned>(a.ctas), (W + NW - 1) / NW));
+        const unsigned workers = nc * NW;
+        share = W / workers;
+        more = W - share * workers;              // the first `more` warps take one tile more
+        const unsigned id = cta * NW + warp;
+        t0 = share * id + min(id, more);
+        my_n = id < workers ? share + (id < more ? 1 : 0) : 0;
         unsigned base = 0;
-        for (int r0 = 0; r0 < a.B; r0 += 32) {
+        for (int r0 = 0; my_n > 0 && r0 < a.B; r0 += 32) {
             const int n = r0 == 0 ? n_lane : r0 + lane < a.B ? row_len(r0 + lane) : 0;
             const int own = r0 == 0 ? tiles_lane : row_tiles(n);
             unsigned incl = static_cast<unsigned>(own) * a.Hkv;
@@ -212,22 +238,15 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     int wphys = -1, wlog = -1;
     bool wvalid = false;
     auto load_window = [&](int first) {
-        wbase = first;
+        wbase = early ? 0 : first;
         wphys = wlog = -1;
-        const int held = (ic.n + ps - 1) >> a.page_shift;
-        if (first + lane < row_blocks(ic.n)) {
-            int lg = first + lane;
-            if (a.sel != nullptr) lg = a.sel[(static_cast<size_t>(ic.b) * a.Hkv + ic.j) * a.top + lg];
-            if (lg >= 0 && lg < held) {
-                wlog = lg;
-                const int ph = a.table[static_cast<size_t>(ic.b) * a.max_blocks + lg];
-                if (ph >= 0 && ph < a.num_pages)
-                    wphys = ph;
-                else
-                    atomicOr(a.err, ERR_RANGE);
-            } else {
-                atomicOr(a.err, ERR_RANGE);
-            }
+        const int held = (ic.n + ps - 1) >> a.page_shift, i = wbase + lane;
+        if (i < row_blocks(ic.n)) {
+            int lg = early_lg, ph = early_ph;
+            if (!early) look_up(ic.b, ic.j, i, lg, ph);
+            if (lg >= 0 && lg < held) wlog = lg;
+            if (wlog >= 0 && ph >= 0 && ph < a.num_pages) wphys = ph;
+            if (wphys < 0) atomicOr(a.err, ERR_RANGE);       // a block or a page that does not exist
         }
         wvalid = true;
     };
@@ -496,7 +515,15 @@ cudaError_t launch_paged(const CUtensorMap& tmK, const CUtensorMap& tmV, const P
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (e != cudaSuccess) return e;
-    return launch_kernel(kern, dim3(a.ctas), dim3(P::NW * 32), smem, st, true, tmK, tmV, a);
+    // One CTA per unit where the units fit the grid and even the longest possible one is short:
+    // joining a unit across CTAs costs about as much as 4 tiles of every warp. With most of the
+    // multiprocessors busy anyway twice that is worth it (one 320-token request: 8.8 -> 7.0 us;
+    // 32 ragged requests of up to 2K: 15.4 -> 14.8 us; but 8 units of 1K tokens: 19.2 -> 22.0 us).
+    PagedDecodeArgs args = a;
+    const int units = a.B * a.Hkv;
+    const long long cap = static_cast<long long>(a.sel != nullptr ? std::min(a.top, a.max_blocks) : a.max_blocks) << a.page_shift;
+    args.aligned = units <= a.ctas && cap <= static_cast<long long>(P::NW) * P::TT * (2 * units >= a.ctas ? 8 : 4);
+    return launch_kernel(kern, dim3(args.aligned ? units : a.ctas), dim3(P::NW * 32), smem, st, true, tmK, tmV, args);
 }
 
 // The deepest ring that fits beside the saved states and scratch, at most three stages.

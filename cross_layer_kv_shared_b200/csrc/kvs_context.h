@@ -84,11 +84,10 @@ struct kvshare_ctx {
     float* sscore = nullptr;
     // projected queries of one low-rank prefill layer [max_batch][Hq][max_context][64] bf16
     uint16_t* qp = nullptr;
-    // paged cache: split partials (two per CTA), arrival counters (one per CTA, zero between
-    // launches), and page scores [max_batch][Hkv][max blocks] of the block selection
+    // paged cache: split partials (two per CTA) and arrival counters (one per CTA and one for
+    // planning, zero between launches)
     float* pg_ws = nullptr;
     unsigned* pg_counters = nullptr;
-    float* pg_score = nullptr;
     // staging for kvshare_decode_host
     void* q_stage = nullptr;
     float* out_stage = nullptr;

@@ -32,6 +32,7 @@ struct PagedDecodeArgs {
     unsigned* err;
     long long wait_limit;
     int ctas;               // grid: at most one CTA per SM
+    int aligned;            // one CTA per unit (set by the launcher)
 };
 // rows of the K/V tensor-map boxes (tokens per copy)
 int decode_paged_box_rows(bool f32, int d, bool mix, int page_size);
@@ -52,16 +53,16 @@ struct PagedSelectArgs {
     const int* table;
     const int* lens;
     const float* w;             // [Hkv], MIX only
-    float* score;               // [B][Hkv][max_blocks] workspace
     int* sel;                   // [B][Hkv][top]
     int src0, src1;
     int B, Hq, Hkv, g, d;
     int num_pages, max_blocks, page_shift, top, first, last;
+    int cluster;                // CTAs per (sequence, kv head), set by the launcher
     bool f32, mix;
     unsigned* err;
 };
 constexpr int SELECT_MAX_BLOCKS = 16384;
-int launch_select_pages(const PagedSelectArgs& a, cudaStream_t st);   // kernels launched, or -1
+cudaError_t launch_select_pages(const PagedSelectArgs& a, int sms, cudaStream_t st);
 
 // Append of new tokens to one slot.
 struct PagedAppendArgs {

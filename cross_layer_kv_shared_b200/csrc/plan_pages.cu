@@ -20,26 +20,44 @@ namespace kvs {
 namespace {
 
 constexpr int NT = 1024;
-constexpr int E = PLAN_MAX_BATCH / NT;
 
-template <typename T>
-__device__ T block_scan(T v, T* warp_sums) {         // exclusive prefix sum over the block
+// prefix sums saturate here: they only have to tell what exceeds 32-bit limits
+__device__ __forceinline__ unsigned sat(unsigned a, unsigned b) { return min(a + b, 0x7fffffffu); }
+
+// exclusive prefix sums over the block of N values at once; `sums` is [N][32], one per use
+template <int N>
+__device__ __forceinline__ void block_scan(unsigned (&v)[N], unsigned (*sums)[32]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    T incl = v;
+    unsigned incl[N];
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const T x = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += x;
+    for (int i = 0; i < N; ++i) incl[i] = v[i];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const unsigned x = __shfl_up_sync(0xffffffffu, incl[i], off);
+            if (lane >= off) incl[i] = sat(incl[i], x);
+        }
+    if (lane == 31)
+#pragma unroll
+        for (int i = 0; i < N; ++i) sums[i][warp] = incl[i];
+    __syncthreads();
+    unsigned base[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) base[i] = lane < warp ? sums[i][lane] : 0u;    // 32 warps: the sums before this one
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) base[i] = sat(base[i], __shfl_xor_sync(0xffffffffu, base[i], off));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const unsigned before = __shfl_up_sync(0xffffffffu, incl[i], 1);
+        v[i] = sat(base[i], lane > 0 ? before : 0u);
     }
-    if (lane == 31) warp_sums[warp] = incl;
-    __syncthreads();
-    T base = lane < warp ? warp_sums[lane] : T(0);   // 32 warps: each adds up those before it
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) base += __shfl_xor_sync(0xffffffffu, base, off);
-    __syncthreads();
-    return base + incl - v;
 }
 
+// E: sequences per thread
+template <int E>
 __global__ void __launch_bounds__(NT) plan_pages_kernel(const PagePlanArgs a) {
     extern __shared__ int sm[];
     int* s_start = sm;                    // [B + 1] first token
@@ -47,8 +65,7 @@ __global__ void __launch_bounds__(NT) plan_pages_kernel(const PagePlanArgs a) {
     int* s_new = s_len + a.B;             // [B] new pages of earlier sequences
     int* s_back = s_new + a.B;            // [B] returning pages
     int* s_backx = s_back + a.B;          // [B] returning pages of earlier sequences
-    __shared__ long long wsum[32];
-    __shared__ int wsum32[32];
+    __shared__ unsigned s_sum[5][32];
     __shared__ int s_total[3];            // tokens, new pages, returning pages
     __shared__ bool s_last;
     grid_dep_wait();
@@ -63,15 +80,15 @@ __global__ void __launch_bounds__(NT) plan_pages_kernel(const PagePlanArgs a) {
         count = 0;                        // an unusable ring has no free page
     }
     int n[E], held[E];
-    long long want[E], need[E];
+    unsigned want[E], need[E];
     bool leaves[E];
-    long long sum_want = 0, sum_need = 0;
+    unsigned at[2] = {0u, 0u};            // tokens wanted and pages needed, first of this thread's, then before them
     unsigned err = 0u;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         const int b = threadIdx.x * E + e;
         n[e] = held[e] = 0;
-        want[e] = need[e] = 0;
+        want[e] = need[e] = 0u;
         leaves[e] = false;
         if (b < a.B) {
             int len = a.lens[b];
@@ -92,35 +109,36 @@ __global__ void __launch_bounds__(NT) plan_pages_kernel(const PagePlanArgs a) {
                 }
             }
         }
-        sum_want += want[e];
-        sum_need += need[e];
+        at[0] = sat(at[0], want[e]);
+        at[1] = sat(at[1], need[e]);
     }
-    long long at_want = block_scan(sum_want, wsum);      // also: every input of this block is read
-    if (gridDim.x > 1 && threadIdx.x == 0) {
-        unsigned prev;
-        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(prev) : "l"(a.counter) : "memory");
-        s_last = prev == gridDim.x - 1;
-        if (s_last) *a.counter = 0u;
-    } else if (threadIdx.x == 0) {
+    block_scan(at, s_sum);                // its barrier: every input of this block is read
+    if (threadIdx.x == 0) {
+        s_total[2] = 0;
         s_last = true;
+        if (gridDim.x > 1) {
+            unsigned prev;
+            asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(prev) : "l"(a.counter) : "memory");
+            s_last = prev == gridDim.x - 1;
+            if (s_last) *a.counter = 0u;
+        }
     }
-    long long at_need = block_scan(sum_need, wsum);
-    int got[E], sum_got = 0, sum_new = 0, sum_held = 0;
+    int got[E];
+    unsigned sums[3] = {0u, 0u, 0u};      // tokens taken, new pages, pages of those that leave
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        at_want += want[e];
-        at_need += need[e];
-        const bool ok = (need[e] == 0 || at_need <= count) && at_want <= a.max_tokens;
-        if (!ok && want[e] > 0) err |= ERR_POOL;
+        at[0] = sat(at[0], want[e]);
+        at[1] = sat(at[1], need[e]);
+        const bool ok = (need[e] == 0u || at[1] <= static_cast<unsigned>(count)) && at[0] <= static_cast<unsigned>(a.max_tokens);
+        if (!ok && want[e] > 0u) err |= ERR_POOL;
         got[e] = ok ? static_cast<int>(want[e]) : 0;
-        if (!ok) need[e] = 0;
-        sum_got += got[e];
-        sum_new += static_cast<int>(need[e]);
-        sum_held += leaves[e] ? held[e] : 0;             // at most B * max_blocks, checked by the caller
+        if (!ok) need[e] = 0u;
+        sums[0] += got[e];
+        sums[1] += need[e];
+        sums[2] += leaves[e] ? held[e] : 0;              // at most B * max_blocks, checked by the caller
     }
-    int at_got = block_scan(sum_got, wsum32);
-    int at_new = block_scan(sum_new, wsum32);
-    int at_back = block_scan(sum_held, wsum32);
+    block_scan(sums, s_sum + 2);
+    int at_got = sums[0], at_new = sums[1], at_back = sums[2];
     const int room = bad_ring ? 0 : a.num_pages - count;
     int sum_back = 0;
 #pragma unroll
@@ -145,8 +163,6 @@ __global__ void __launch_bounds__(NT) plan_pages_kernel(const PagePlanArgs a) {
             s_total[1] = at_new;
         }
     }
-    if (threadIdx.x == 0) s_total[2] = 0;
-    __syncthreads();
     if (sum_back > 0) atomicAdd(&s_total[2], sum_back);
     if (err != 0u && blockIdx.x == 0) atomicOr(a.err, err);
     __syncthreads();
@@ -202,18 +218,22 @@ __global__ void __launch_bounds__(NT) plan_pages_kernel(const PagePlanArgs a) {
 
 }  // namespace
 
-cudaError_t launch_plan_pages(const PagePlanArgs& a, int sms, cudaStream_t st) {
-    const int smem = (5 * a.B + 1) * 4;
+template <int E>
+static cudaError_t launch(const PagePlanArgs& a, int blocks, cudaStream_t st) {
+    auto kern = plan_pages_kernel<E>;
     static std::atomic<unsigned long long> attr_done{0};
     cudaError_t e = once_per_device(attr_done, [&] {
-        return cudaFuncSetAttribute(plan_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (5 * PLAN_MAX_BATCH + 1) * 4);
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (5 * NT * E + 1) * 4);
     });
     if (e != cudaSuccess) return e;
+    return launch_kernel(kern, dim3(blocks), dim3(NT), (5 * a.B + 1) * 4, st, true, a);
+}
+
+cudaError_t launch_plan_pages(const PagePlanArgs& a, int sms, cudaStream_t st) {
+    static_assert(PLAN_MAX_BATCH <= 4 * NT, "sequences of a block");
     int blocks = (a.max_tokens + NT - 1) / NT;
     if (blocks > sms) blocks = sms;
-    if (blocks < 1) blocks = 1;
-    return launch_kernel(plan_pages_kernel, dim3(blocks), dim3(NT), smem, st, true, a);
+    return a.B <= NT ? launch<1>(a, blocks, st) : launch<4>(a, blocks, st);
 }
 
 }  // namespace kvs

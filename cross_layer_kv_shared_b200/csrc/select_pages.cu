@@ -9,22 +9,26 @@
 // (below 2^22, exact in fp32 whatever the order), and every fp32 step after it is one IEEE
 // operation, so the selection is reproducible bit for bit.
 //
-// select_score: bound by the codes' bytes (2 d + 4 per page and head). A warp takes 16 pages
-// of a head: each lane reads 16-byte pieces of two pages' codes straight into the fragments
-// of mma.sync m16n8k32 s8 (the product's index may be permuted freely as long as the query
-// codes are laid out alike), the group's heads are its columns.
-// select_top: one block per (sequence, kv head), bound by latency. Scores become ordered
-// 32-bit keys in registers; the top-th largest is found bit by bit (a count over the block
-// each), then the kept blocks are written in ascending order by a prefix sum. Ties go to the
-// lowest block; the first and last blocks asked for are kept whatever their score.
+// One cluster of 1 to 8 CTAs per (sequence, kv head). Scores: bound by the codes' bytes
+// (2 d + 4 per page). A warp takes 16 pages: each lane reads 16-byte pieces of two pages' codes
+// straight into the fragments of mma.sync m16n8k32 s8 (the product's index may be permuted
+// freely as long as the query codes are laid out alike), the group's heads are its columns.
+// The scores, as ordered 32-bit keys, go into the first CTA's shared memory (distributed shared
+// memory from the others), so they never travel to L2 and no second launch waits for them.
+// Choice: bound by latency, in the first CTA. The keys move to registers; the top-th largest is
+// found bit by bit from the highest bit that differs, a count over the block each, ending as
+// soon as exactly `top` keys are at or above the candidate; the kept blocks are written in
+// ascending order by a prefix sum. Ties go to the lowest block; the first and last blocks asked
+// for are kept whatever their score.
 #include "kvs_device.cuh"
 #include "kvs_paged.h"
 
 namespace kvs {
 namespace {
 
-constexpr int SCORE_WARPS = 8;
-constexpr int SCORE_PAGES = SCORE_WARPS * 16;
+constexpr int NT = 512;
+constexpr int NWARP = NT / 32;
+constexpr int MAX_CLUSTER = 8;
 
 __device__ __forceinline__ void mma_s8(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -42,20 +46,53 @@ __device__ __forceinline__ int seq_tokens(const PagedSelectArgs& a, int b) {
     return n;
 }
 
-template <int D, bool F32, bool MIX, int NH>
-__global__ void __launch_bounds__(SCORE_WARPS * 32) select_score_kernel(const PagedSelectArgs a) {
+// An unsigned key in the order of the scores, above 0; NaN below every number.
+__device__ __forceinline__ uint32_t score_key(float s) {
+    if (s != s) return 1u;
+    const uint32_t u = __float_as_uint(s == 0.f ? 0.f : s);     // -0 and 0 tie
+    return max((u & 0x80000000u) ? ~u : (u | 0x80000000u), 1u);
+}
+
+// the address of `p` (own shared memory) in the shared memory of the cluster's CTA 0
+__device__ __forceinline__ uint32_t in_first_cta(const void* p) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// E: keys per thread of the choosing CTA
+template <int D, bool F32, bool MIX, int NH, int E>
+__global__ void __launch_bounds__(NT) select_pages_kernel(const PagedSelectArgs a) {
     constexpr int NB = NH / 8;
     constexpr int PIECES = 2 * D / 64;              // 64-byte steps of a page's codes
+    extern __shared__ uint32_t s_key[];             // [blocks] (CTA 0's is the one used)
     __shared__ __align__(16) int8_t s_code[NH][2 * D];
     __shared__ float s_scale[NH];
-    const int b = blockIdx.z, j = blockIdx.y;
+    __shared__ int s_cnt[2][NWARP];
+    __shared__ uint32_t s_mm[2][NWARP];
+    const int C = a.cluster, rank = C > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int unit = blockIdx.x / C, b = unit / a.Hkv, j = unit - b * a.Hkv;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_dep_wait();
     if (threadIdx.x == 0) grid_dep_launch();
     const int held = (seq_tokens(a, b) + (1 << a.page_shift) - 1) >> a.page_shift;
-    if (static_cast<int>(blockIdx.x) * SCORE_PAGES >= held) return;
+    int* out = a.sel + static_cast<size_t>(unit) * a.top;
+    if (held <= a.top) {                            // every block, whatever its score (the whole cluster)
+        if (rank == 0)
+            for (int i = threadIdx.x; i < a.top; i += NT) out[i] = i < held ? i : -1;
+        return;
+    }
     // ---- the group's query codes, positive part then negative part
-    for (int h = warp; h < NH; h += SCORE_WARPS) {
+    for (int h = warp; h < NH; h += NWARP) {
         constexpr int PER = D / 32;
         float v[PER];
         float top = 0.f;
@@ -77,112 +114,105 @@ __global__ void __launch_bounds__(SCORE_WARPS * 32) select_score_kernel(const Pa
         }
         if (lane == 0) s_scale[h] = s;
     }
-    __syncthreads();
-    const int p0 = blockIdx.x * SCORE_PAGES + warp * 16;
-    if (p0 >= held) return;
-    // ---- pages p0 + lane / 4 and + 8
+    if (C > 1) cluster_sync();                      // also: CTA 0 runs before its memory is written to
+    else __syncthreads();
+    // ---- scores: 16 pages a warp and step, dealt over the cluster
     const int r = lane >> 2, c4 = lane & 3;
-    int page[2];
-    float score[NB][4];
+    const uint32_t keys0 = C > 1 ? in_first_cta(s_key) : smem_u32(s_key);
+    for (int p0 = (rank * NWARP + warp) * 16; p0 < held; p0 += C * NWARP * 16) {
+        int page[2];
+        float score[NB][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int p = p0 + r + 8 * i;
-        page[i] = p < held ? a.table[static_cast<size_t>(b) * a.max_blocks + p] : -1;
-        if (p < held && (page[i] < 0 || page[i] >= a.num_pages)) {
-            atomicOr(a.err, ERR_RANGE);
-            page[i] = -1;                           // scores as a page of zeros
-        }
-    }
-#pragma unroll
-    for (int src = 0; src < (MIX ? 2 : 1); ++src) {
-        const size_t slot = static_cast<size_t>(src == 0 ? a.src0 : a.src1) * a.num_pages;
-        uint4 x[2][PIECES];
-        float sp[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const size_t row = (slot + max(page[i], 0)) * a.Hkv + j;
-            const uint4* at = reinterpret_cast<const uint4*>(a.codes + row * 2 * D) + c4;
-            sp[i] = page[i] >= 0 ? a.scales[row] : 0.f;
-#pragma unroll
-            for (int k = 0; k < PIECES; ++k) x[i][k] = page[i] >= 0 ? __ldg(at + 4 * k) : make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < 2; ++i) {               // pages p0 + r and + 8
+            const int p = p0 + r + 8 * i;
+            page[i] = p < held ? a.table[static_cast<size_t>(b) * a.max_blocks + p] : -1;
+            if (p < held && (page[i] < 0 || page[i] >= a.num_pages)) {
+                atomicOr(a.err, ERR_RANGE);
+                page[i] = -1;                       // scores as a page of zeros
+            }
         }
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            int acc[4] = {0, 0, 0, 0};
-            const uint4* qc = reinterpret_cast<const uint4*>(s_code[nb * 8 + r]) + c4;
+        for (int src = 0; src < (MIX ? 2 : 1); ++src) {
+            const size_t slot = static_cast<size_t>(src == 0 ? a.src0 : a.src1) * a.num_pages;
+            uint4 x[2][PIECES];
+            float sp[2];
 #pragma unroll
-            for (int k = 0; k < PIECES; ++k) {
-                const uint4 q = qc[4 * k];
-                const uint32_t a0[4] = {x[0][k].x, x[1][k].x, x[0][k].y, x[1][k].y};
-                const uint32_t a1[4] = {x[0][k].z, x[1][k].z, x[0][k].w, x[1][k].w};
-                mma_s8(acc, a0, q.x, q.y);
-                mma_s8(acc, a1, q.z, q.w);
+            for (int i = 0; i < 2; ++i) {
+                const size_t row = (slot + max(page[i], 0)) * a.Hkv + j;
+                const uint4* at = reinterpret_cast<const uint4*>(a.codes + row * 2 * D) + c4;
+                sp[i] = page[i] >= 0 ? a.scales[row] : 0.f;
+#pragma unroll
+                for (int k = 0; k < PIECES; ++k) x[i][k] = page[i] >= 0 ? __ldg(at + 4 * k) : make_uint4(0u, 0u, 0u, 0u);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float s = __fmul_rn(__fmul_rn(static_cast<float>(acc[i]), s_scale[nb * 8 + 2 * c4 + (i & 1)]), sp[i >> 1]);
-                if (!MIX) {
-                    score[nb][i] = s;
-                } else {
-                    const float w = a.w[j];
-                    score[nb][i] = src == 0 ? __fmul_rn(w, s) : __fadd_rn(score[nb][i], __fmul_rn(__fsub_rn(1.f, w), s));
+            for (int nb = 0; nb < NB; ++nb) {
+                int acc[4] = {0, 0, 0, 0};
+                const uint4* qc = reinterpret_cast<const uint4*>(s_code[nb * 8 + r]) + c4;
+#pragma unroll
+                for (int k = 0; k < PIECES; ++k) {
+                    const uint4 q = qc[4 * k];
+                    const uint32_t a0[4] = {x[0][k].x, x[1][k].x, x[0][k].y, x[1][k].y};
+                    const uint32_t a1[4] = {x[0][k].z, x[1][k].z, x[0][k].w, x[1][k].w};
+                    mma_s8(acc, a0, q.x, q.y);
+                    mma_s8(acc, a1, q.z, q.w);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float s = __fmul_rn(__fmul_rn(static_cast<float>(acc[i]), s_scale[nb * 8 + 2 * c4 + (i & 1)]), sp[i >> 1]);
+                    if (!MIX) {
+                        score[nb][i] = s;
+                    } else {
+                        const float w = a.w[j];
+                        score[nb][i] = src == 0 ? __fmul_rn(w, s) : __fadd_rn(score[nb][i], __fmul_rn(__fsub_rn(1.f, w), s));
+                    }
                 }
             }
         }
-    }
-    // ---- the group's largest score of each page
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        float top = NEG_INF;
+        for (int i = 0; i < 2; ++i) {               // the group's largest score of each page
+            float top = NEG_INF;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-                if (nb * 8 + 2 * c4 + k < a.g) top = fmaxf(top, score[nb][2 * i + k]);
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int p = p0 + r + 8 * i;
-        if (c4 == 0 && p < held) a.score[(static_cast<size_t>(b) * a.Hkv + j) * a.max_blocks + p] = top;
+                for (int k = 0; k < 2; ++k)
+                    if (nb * 8 + 2 * c4 + k < a.g) top = fmaxf(top, score[nb][2 * i + k]);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int p = p0 + r + 8 * i;
+            if (c4 == 0 && p < held) {
+                const uint32_t key = p < a.first || p >= held - a.last ? 0xffffffffu : score_key(top);
+                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(keys0 + 4u * p), "r"(key) : "memory");
+            }
+        }
     }
-}
-
-// An unsigned key in the order of the scores; NaN below every number.
-__device__ __forceinline__ uint32_t score_key(float s) {
-    if (s != s) return 0u;
-    const uint32_t u = __float_as_uint(s == 0.f ? 0.f : s);     // -0 and 0 tie
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-
-template <int NT, int E>
-__global__ void __launch_bounds__(NT) select_top_kernel(const PagedSelectArgs a) {
-    constexpr int NWARP = NT / 32;
-    __shared__ int s_cnt[2][NWARP];
-    const int j = blockIdx.x, b = blockIdx.y;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    grid_dep_wait();
-    if (threadIdx.x == 0) grid_dep_launch();
-    const int held = (seq_tokens(a, b) + (1 << a.page_shift) - 1) >> a.page_shift;
-    const size_t row = static_cast<size_t>(b) * a.Hkv + j;
-    int* out = a.sel + row * a.top;
-    if (held <= a.top) {                             // every block
-        for (int i = threadIdx.x; i < a.top; i += NT) out[i] = i < held ? i : -1;
-        return;
-    }
-    // thread t holds blocks t * E .. t * E + E - 1
-    const float* score = a.score + row * a.max_blocks;
+    if (C > 1) cluster_sync();
+    else __syncthreads();
+    if (rank != 0) return;
+    // ---- thread t holds blocks t * E .. t * E + E - 1; 0: no block
     uint32_t key[E];
+    uint32_t hi = 0u, lo = 0xffffffffu;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         const int p = threadIdx.x * E + e;
-        key[e] = 0u;
+        key[e] = p < held ? s_key[p] : 0u;
         if (p < held) {
-            key[e] = max(score_key(__ldcg(score + p)), 1u);     // 0 marks "no block"
-            if (p < a.first || p >= held - a.last) key[e] = 0xffffffffu;
+            hi = max(hi, key[e]);
+            lo = min(lo, key[e]);
         }
     }
-    // the largest T with at least `top` keys >= T, bit by bit
-    uint32_t T = 0u;
-    for (int bit = 31; bit >= 0; --bit) {
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    if (lane == 0) {
+        s_mm[0][warp] = hi;
+        s_mm[1][warp] = lo;
+    }
+    __syncthreads();
+    hi = __reduce_max_sync(0xffffffffu, lane < NWARP ? s_mm[0][lane] : 0u);
+    lo = __reduce_min_sync(0xffffffffu, lane < NWARP ? s_mm[1][lane] : 0xffffffffu);
+    // T: at least `top` keys are >= T. The bits above the highest that differs are common
+    int bit = hi == lo ? -1 : 31 - __clz(hi ^ lo);
+    uint32_t T = hi == lo ? lo : lo & ~((2u << bit) - 1u);
+    for (; bit >= 0; --bit) {
         const uint32_t cand = T | (1u << bit);
         int c = 0;
 #pragma unroll
@@ -190,9 +220,9 @@ __global__ void __launch_bounds__(NT) select_top_kernel(const PagedSelectArgs a)
         c = __reduce_add_sync(0xffffffffu, c);
         if (lane == 0) s_cnt[bit & 1][warp] = c;
         __syncthreads();
-        int all = lane < NWARP ? s_cnt[bit & 1][lane] : 0;
-        all = __reduce_add_sync(0xffffffffu, all);
+        const int all = __reduce_add_sync(0xffffffffu, lane < NWARP ? s_cnt[bit & 1][lane] : 0);
         if (all >= a.top) T = cand;
+        if (all == a.top) break;                    // the same for every thread
     }
     // keep every key above T and the lowest blocks among those equal to it
     int above = 0, equal = 0;
@@ -217,10 +247,9 @@ __global__ void __launch_bounds__(NT) select_top_kernel(const PagedSelectArgs a)
     }
     __syncthreads();
     int wa = lane < NWARP ? s_cnt[0][lane] : 0, we = lane < NWARP ? s_cnt[1][lane] : 0;
-    const int all_above = __reduce_add_sync(0xffffffffu, wa);
+    const int ties = a.top - __reduce_add_sync(0xffffffffu, wa);
     wa = __reduce_add_sync(0xffffffffu, lane < warp ? wa : 0);
     we = __reduce_add_sync(0xffffffffu, lane < warp ? we : 0);
-    const int ties = a.top - all_above;
     int na = wa + ia - above, ne = we + ie - equal;  // kept or tied before this thread's blocks
 #pragma unroll
     for (int e = 0; e < E; ++e) {
@@ -231,35 +260,54 @@ __global__ void __launch_bounds__(NT) select_top_kernel(const PagedSelectArgs a)
     }
 }
 
-template <int D, bool F32, bool MIX>
-cudaError_t launch_score(const PagedSelectArgs& a, cudaStream_t st) {
-    const dim3 grid((a.max_blocks + SCORE_PAGES - 1) / SCORE_PAGES, a.Hkv, a.B);
-    return a.g <= 8 ? launch_kernel(select_score_kernel<D, F32, MIX, 8>, grid, dim3(SCORE_WARPS * 32), 0, st, true, a)
-                    : launch_kernel(select_score_kernel<D, F32, MIX, 16>, grid, dim3(SCORE_WARPS * 32), 0, st, true, a);
+template <int D, bool F32, bool MIX, int NH, int E>
+cudaError_t launch(const PagedSelectArgs& args, int sms, cudaStream_t st) {
+    PagedSelectArgs a = args;
+    auto kern = select_pages_kernel<D, F32, MIX, NH, E>;
+    static std::atomic<unsigned long long> attr_done{0};
+    cudaError_t e = once_per_device(attr_done, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, NT * E * 4);
+    });
+    if (e != cudaSuccess) return e;
+    // CTAs per (sequence, kv head): as many as the multiprocessors allow and the blocks can use
+    const int units = a.B * a.Hkv;
+    a.cluster = 1;
+    while (a.cluster < MAX_CLUSTER && units * a.cluster * 2 <= sms && a.cluster * NWARP * 16 < a.max_blocks) a.cluster *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(units * a.cluster);
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = static_cast<size_t>(a.max_blocks) * 4;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+template <int D, bool F32, bool MIX, int NH>
+cudaError_t launch_e(const PagedSelectArgs& a, int sms, cudaStream_t st) {
+    if (a.max_blocks <= 2 * NT) return launch<D, F32, MIX, NH, 2>(a, sms, st);
+    if (a.max_blocks <= 8 * NT) return launch<D, F32, MIX, NH, 8>(a, sms, st);
+    return launch<D, F32, MIX, NH, 32>(a, sms, st);
 }
 
 template <bool F32, bool MIX>
-cudaError_t launch_score_d(const PagedSelectArgs& a, cudaStream_t st) {
-    return a.d == 64 ? launch_score<64, F32, MIX>(a, st) : launch_score<128, F32, MIX>(a, st);
+cudaError_t launch_d(const PagedSelectArgs& a, int sms, cudaStream_t st) {
+    if (a.d == 64) return a.g <= 8 ? launch_e<64, F32, MIX, 8>(a, sms, st) : launch_e<64, F32, MIX, 16>(a, sms, st);
+    return a.g <= 8 ? launch_e<128, F32, MIX, 8>(a, sms, st) : launch_e<128, F32, MIX, 16>(a, sms, st);
 }
 
 }  // namespace
 
-int launch_select_pages(const PagedSelectArgs& a, cudaStream_t st) {
-    int launched = 0;
-    if (a.max_blocks > a.top) {                      // otherwise every block is kept, whatever its score
-        const cudaError_t e = a.f32 ? (a.mix ? launch_score_d<true, true>(a, st) : launch_score_d<true, false>(a, st))
-                                    : (a.mix ? launch_score_d<false, true>(a, st) : launch_score_d<false, false>(a, st));
-        if (e != cudaSuccess) return -1;
-        ++launched;
-    }
-    const dim3 grid(a.Hkv, a.B);
-    cudaError_t e;
-    if (a.max_blocks <= 1024) e = launch_kernel(select_top_kernel<256, 4>, grid, dim3(256), 0, st, true, a);
-    else if (a.max_blocks <= 4096) e = launch_kernel(select_top_kernel<512, 8>, grid, dim3(512), 0, st, true, a);
-    else e = launch_kernel(select_top_kernel<1024, 16>, grid, dim3(1024), 0, st, true, a);
-    if (e != cudaSuccess) return -1;
-    return launched + 1;
+cudaError_t launch_select_pages(const PagedSelectArgs& a, int sms, cudaStream_t st) {
+    static_assert(SELECT_MAX_BLOCKS <= 32 * NT, "keys of the longest list");
+    if (a.f32) return a.mix ? launch_d<true, true>(a, sms, st) : launch_d<true, false>(a, sms, st);
+    return a.mix ? launch_d<false, true>(a, sms, st) : launch_d<false, false>(a, sms, st);
 }
 
 }  // namespace kvs
