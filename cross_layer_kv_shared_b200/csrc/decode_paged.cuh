@@ -399,32 +399,44 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         for (int c = k / VALS; c > 0; --c) rest &= rest - 1u;
         const int i = __ffs(rest) - 1;
         const unsigned states = states_from(i);
-        // two states at a time, their loads together (a missing second one is the first, weight 0)
+        // four states at a time, their loads together (missing ones repeat the first with weight 0)
+        auto next4 = [](unsigned& r, int (&q)[4]) {
+            int n = 0;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                q[x] = r != 0u ? __ffs(r) - 1 : q[0];
+                n += r != 0u ? 1 : 0;
+                r &= r - 1u;
+            }
+            return n;
+        };
         float2 M = make_float2(NEG_INF, NEG_INF);
+        int q[4];
         for (unsigned r = states; r != 0u;) {
-            const int s0 = __ffs(r) - 1;
-            r &= r - 1u;
-            const int s1 = r ? __ffs(r) - 1 : s0;
-            r &= r - 1u;
-            M.x = fmaxf(M.x, fmaxf(s_ml[s0][hd.x].x, s_ml[s1][hd.x].x));
-            M.y = fmaxf(M.y, fmaxf(s_ml[s0][hd.y].x, s_ml[s1][hd.y].x));
+            next4(r, q);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                M.x = fmaxf(M.x, s_ml[q[x]][hd.x].x);
+                M.y = fmaxf(M.y, s_ml[q[x]][hd.y].x);
+            }
         }
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         float2 l = make_float2(0.f, 0.f);
-        // odd states lie over their warp's ring, even ones in the save area
-        auto value = [&](int s) {
-            return reinterpret_cast<const float4*>(smem + ((s & 1) ? (s >> 1) * NSW * P::STAGE : L::RING + (s >> 1) * VALS * 16))[idx];
-        };
         for (unsigned r = states; r != 0u;) {
-            const int s0 = __ffs(r) - 1;
-            r &= r - 1u;
-            const bool two = r != 0u;
-            const int s1 = two ? __ffs(r) - 1 : s0;
-            r &= r - 1u;
-            const float4 v0 = value(s0), v1 = value(s1);
-            const float2 x0 = s_ml[s0][hd.x], y0 = s_ml[s0][hd.y], x1 = s_ml[s1][hd.x], y1 = s_ml[s1][hd.y];
-            add_state(acc, l, v0, x0, y0, M);
-            if (two) add_state(acc, l, v1, x1, y1, M);
+            const int n = next4(r, q);
+            float4 v[4];
+            float2 mx[4], my[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                // odd states lie over their warp's ring, even ones in the save area
+                v[x] = reinterpret_cast<const float4*>(
+                    smem + ((q[x] & 1) ? (q[x] >> 1) * NSW * P::STAGE : L::RING + (q[x] >> 1) * VALS * 16))[idx];
+                mx[x] = s_ml[q[x]][hd.x];
+                my[x] = s_ml[q[x]][hd.y];
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (x < n) add_state(acc, l, v[x], mx[x], my[x], M);
         }
         if ((splits >> i) & 1u) {
             float* part = a.ws + static_cast<size_t>(2 * cta + s_state[i].started) * per;

@@ -68,11 +68,12 @@ struct PagedBf16 {
         float sc[MT][NB][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            float s2[NB][4];
+            // even and odd channel steps accumulate apart: half the chain of dependent products
+            float s1[2][NB][4], s2[2][NB][4];
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sc[mt][nb][i] = s2[nb][i] = 0.f;
+                for (int i = 0; i < 4; ++i) s1[0][nb][i] = s1[1][nb][i] = s2[0][nb][i] = s2[1][nb][i] = 0.f;
             const int row = (mi & 1) * 8 + ri;
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
@@ -81,19 +82,20 @@ struct PagedBf16 {
                 uint32_t af[4];
                 ldsm_x4(kb + off, af[0], af[1], af[2], af[3]);
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) mma_bf16(sc[mt][nb], af, qb[ks][nb][0], qb[ks][nb][1]);
+                for (int nb = 0; nb < NB; ++nb) mma_bf16(s1[ks & 1][nb], af, qb[ks][nb][0], qb[ks][nb][1]);
                 if (MIX) {
                     ldsm_x4(kb + 2 * TILE_BYTES + off, af[0], af[1], af[2], af[3]);
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) mma_bf16(s2[nb], af, qb[ks][nb][0], qb[ks][nb][1]);
+                    for (int nb = 0; nb < NB; ++nb) mma_bf16(s2[ks & 1][nb], af, qb[ks][nb][0], qb[ks][nb][1]);
                 }
             }
-            if (MIX) {
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[mt][nb][i] = fmaf(w, sc[mt][nb][i], w1 * s2[nb][i]);
-            }
+                for (int i = 0; i < 4; ++i) {
+                    sc[mt][nb][i] = s1[0][nb][i] + s1[1][nb][i];
+                    if (MIX) sc[mt][nb][i] = fmaf(w, sc[mt][nb][i], w1 * (s2[0][nb][i] + s2[1][nb][i]));
+                }
             if (cut) {
                 const int end = lim[mt] - (lane >> 2);    // rows r of this lane are tokens iff r < end
 #pragma unroll
