@@ -538,9 +538,9 @@ cudaError_t launch_paged(const CUtensorMap& tmK, const CUtensorMap& tmV, const P
     return launch_kernel(kern, dim3(args.aligned ? units : a.ctas), dim3(P::NW * 32), smem, st, true, tmK, tmV, args);
 }
 
-// The deepest ring that fits beside the saved states and scratch, at most three stages.
+// The deepest ring that fits beside the saved states and scratch, at most two stages.
 constexpr int paged_stages(int nw, int stage, int nh, int d, int warp_floats) {
-    for (int s = 3; s > 1; --s)
+    for (int s = 2; s > 1; --s)
         if (nw * (s * stage + nh * d * 4 + warp_floats * 4) + 1024 <= PAGED_SMEM_MAX) return s;
     return 1;
 }

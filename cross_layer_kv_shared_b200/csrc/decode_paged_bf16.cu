@@ -21,7 +21,11 @@ struct PagedBf16 {
     static constexpr int TT = D == 128 ? 16 : 32;
     static constexpr int SUBW = 64;
     static constexpr int STAGE = 2 * NSRC * TT * D * 2;
-    static constexpr int NW = STAGE <= 8192 ? 8 : 4;
+    // many warps with short rings: a tile's chain of dependent products takes longer than its
+    // share of HBM time, so warps hide it (d = 128 mix: 60 us with 4 x 3 stages, 55.5 with 8 x 1;
+    // d = 64: 15.1 us with 8 x 3, 14.6 with 8 x 2, 13.9 with 12 x 2; d = 128: 120.5 us with 8 x 2,
+    // 125 with 10 x 2, 131 with 8 x 1)
+    static constexpr int NW = !MIX && D == 64 && NH == 8 ? 12 : 8;
     static constexpr int WARP_FLOATS = 0;
     static constexpr int NSW = paged_stages(NW, STAGE, NH, D, WARP_FLOATS);
     static constexpr int MT = TT / 16, NB = NH / 8, TILE_BYTES = TT * D * 2;

@@ -19,7 +19,7 @@ struct PagedF32 {
     static constexpr int TT = 16;
     static constexpr int SUBW = 32;
     static constexpr int STAGE = 2 * NSRC * TT * D * 4;
-    static constexpr int NW = STAGE <= 8192 ? 8 : STAGE <= 16384 ? 4 : 2;
+    static constexpr int NW = STAGE <= 8192 || (STAGE <= 16384 && NH <= 8) ? 8 : 4;
     static constexpr int QF = NH * D;                     // queries of the unit
     static constexpr int WARP_FLOATS = QF + TT * NH + NH; // + weights [TT][NH] + corrections [NH]
     static constexpr int NSW = paged_stages(NW, STAGE, NH, D, WARP_FLOATS);
