@@ -479,7 +479,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         const float* base = a.ws + static_cast<size_t>(2 * c0) * per;
         auto slot = [&](int i) { return base + (2 * i + (i == 0 ? 1 : 0)) * per; };
         // a thread's first values are on their way while the statistics are shared
-        constexpr int AHEAD = 4;
+        constexpr int AHEAD = 8;
         float4 early[AHEAD];
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i)
@@ -504,7 +504,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                 for (; i < AHEAD; ++i)
                     if (i < n) add_state(acc, l, early[i], stat[i * NH + hd.x], stat[i * NH + hd.y], M);
             }
-#pragma unroll 4
+#pragma unroll 8
             for (; i < n; ++i)
                 add_state(acc, l, __ldcg(reinterpret_cast<const float4*>(slot(i)) + idx), stat[i * NH + hd.x], stat[i * NH + hd.y], M);
             P::emit(a.out + static_cast<size_t>(head0) * D, g, idx, acc, make_float2(inverse_of(l.x), inverse_of(l.y)));

@@ -77,13 +77,32 @@ __global__ void __launch_bounds__(NT) select_pages_kernel(const PagedSelectArgs 
     extern __shared__ uint32_t s_key[];             // [blocks] (CTA 0's is the one used)
     __shared__ __align__(16) int8_t s_code[NH][2 * D];
     __shared__ float s_scale[NH];
-    __shared__ int s_cnt[2][NWARP];
+    __shared__ uint2 s_cnt[2][NWARP];
     __shared__ uint32_t s_mm[2][NWARP];
     const int C = a.cluster, rank = C > 1 ? static_cast<int>(cluster_rank()) : 0;
     const int unit = blockIdx.x / C, b = unit / a.Hkv, j = unit - b * a.Hkv;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_dep_wait();
     if (threadIdx.x == 0) grid_dep_launch();
+    // the first step's pages and this warp's query are on their way beside the length
+    const int r = lane >> 2, c4 = lane & 3;
+    const int* table = a.table + static_cast<size_t>(b) * a.max_blocks;
+    int first_page[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int p = (rank * NWARP + warp) * 16 + r + 8 * i;
+        first_page[i] = p < a.max_blocks ? table[p] : -1;
+    }
+    constexpr int PER = D / 32;
+    float v[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        v[i] = 0.f;
+        const size_t at = (static_cast<size_t>(b) * a.Hq + static_cast<size_t>(j) * a.g + warp) * D + lane * PER + i;
+        if (warp < a.g)
+            v[i] = F32 ? static_cast<const float*>(a.q)[at]
+                       : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(a.q)[at]) << 16);
+    }
     const int held = (seq_tokens(a, b) + (1 << a.page_shift) - 1) >> a.page_shift;
     int* out = a.sel + static_cast<size_t>(unit) * a.top;
     if (held <= a.top) {                            // every block, whatever its score (the whole cluster)
@@ -92,40 +111,32 @@ __global__ void __launch_bounds__(NT) select_pages_kernel(const PagedSelectArgs 
         return;
     }
     // ---- the group's query codes, positive part then negative part
-    for (int h = warp; h < NH; h += NWARP) {
-        constexpr int PER = D / 32;
-        float v[PER];
+    static_assert(NH <= NWARP, "a warp per head");
+    if (warp < NH) {
         float top = 0.f;
-        const size_t at = (static_cast<size_t>(b) * a.Hq + static_cast<size_t>(j) * a.g + h) * D + lane * PER;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            v[i] = 0.f;
-            if (h < a.g)
-                v[i] = F32 ? static_cast<const float*>(a.q)[at + i]
-                           : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(a.q)[at + i]) << 16);
-            top = fmaxf(top, fabsf(v[i]));
-        }
+        for (int i = 0; i < PER; ++i) top = fmaxf(top, fabsf(v[i]));
         const float s = __fmul_rn(warp_max(top), INV_127);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int c = s > 0.f ? __float2int_rn(__fdiv_rn(v[i], s)) : 0;
-            s_code[h][lane * PER + i] = static_cast<int8_t>(max(c, 0));
-            s_code[h][D + lane * PER + i] = static_cast<int8_t>(min(c, 0));
+            s_code[warp][lane * PER + i] = static_cast<int8_t>(max(c, 0));
+            s_code[warp][D + lane * PER + i] = static_cast<int8_t>(min(c, 0));
         }
-        if (lane == 0) s_scale[h] = s;
+        if (lane == 0) s_scale[warp] = s;
     }
     if (C > 1) cluster_sync();                      // also: CTA 0 runs before its memory is written to
     else __syncthreads();
     // ---- scores: 16 pages a warp and step, dealt over the cluster
-    const int r = lane >> 2, c4 = lane & 3;
     const uint32_t keys0 = C > 1 ? in_first_cta(s_key) : smem_u32(s_key);
-    for (int p0 = (rank * NWARP + warp) * 16; p0 < held; p0 += C * NWARP * 16) {
+    const int begin = (rank * NWARP + warp) * 16;
+    for (int p0 = begin; p0 < held; p0 += C * NWARP * 16) {
         int page[2];
         float score[NB][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {               // pages p0 + r and + 8
             const int p = p0 + r + 8 * i;
-            page[i] = p < held ? a.table[static_cast<size_t>(b) * a.max_blocks + p] : -1;
+            page[i] = p >= held ? -1 : p0 == begin ? first_page[i] : table[p];
             if (p < held && (page[i] < 0 || page[i] >= a.num_pages)) {
                 atomicOr(a.err, ERR_RANGE);
                 page[i] = -1;                       // scores as a page of zeros
@@ -212,17 +223,27 @@ __global__ void __launch_bounds__(NT) select_pages_kernel(const PagedSelectArgs 
     // T: at least `top` keys are >= T. The bits above the highest that differs are common
     int bit = hi == lo ? -1 : 31 - __clz(hi ^ lo);
     uint32_t T = hi == lo ? lo : lo & ~((2u << bit) - 1u);
-    for (; bit >= 0; --bit) {
-        const uint32_t cand = T | (1u << bit);
-        int c = 0;
+    // two bits a step: the counts of the three candidates, two of them in one word
+    bool found = false;
+    for (int step = 0; bit >= 0 && !found; bit -= 2, ++step) {
+        const int low = bit > 0 ? bit - 1 : 0;
+        const uint32_t unit_k = 1u << low, c1 = T + unit_k, c2 = bit > 0 ? T + 2u * unit_k : c1, c3 = bit > 0 ? T + 3u * unit_k : c1;
+        unsigned n12 = 0u, n3 = 0u;
 #pragma unroll
-        for (int e = 0; e < E; ++e) c += key[e] >= cand ? 1 : 0;
-        c = __reduce_add_sync(0xffffffffu, c);
-        if (lane == 0) s_cnt[bit & 1][warp] = c;
+        for (int e = 0; e < E; ++e) {
+            n12 += (key[e] >= c1 ? 1u : 0u) + (key[e] >= c2 ? 0x10000u : 0u);
+            n3 += key[e] >= c3 ? 1u : 0u;
+        }
+        n12 = __reduce_add_sync(0xffffffffu, n12);
+        n3 = __reduce_add_sync(0xffffffffu, n3);
+        if (lane == 0) s_cnt[step & 1][warp] = make_uint2(n12, n3);
         __syncthreads();
-        const int all = __reduce_add_sync(0xffffffffu, lane < NWARP ? s_cnt[bit & 1][lane] : 0);
-        if (all >= a.top) T = cand;
-        if (all == a.top) break;                    // the same for every thread
+        const uint2 own = lane < NWARP ? s_cnt[step & 1][lane] : make_uint2(0u, 0u);
+        const unsigned a12 = __reduce_add_sync(0xffffffffu, own.x), top = a.top;
+        const unsigned k1 = a12 & 0xffffu, k2 = a12 >> 16, k3 = __reduce_add_sync(0xffffffffu, own.y);
+        const unsigned got = k3 >= top ? k3 : k2 >= top ? k2 : k1;
+        T = k3 >= top ? c3 : k2 >= top ? c2 : k1 >= top ? c1 : T;
+        found = got == top;                         // exactly the wanted blocks: the same for every thread
     }
     // keep every key above T and the lowest blocks among those equal to it
     int above = 0, equal = 0;
@@ -241,12 +262,10 @@ __global__ void __launch_bounds__(NT) select_pages_kernel(const PagedSelectArgs 
         }
     }
     __syncthreads();
-    if (lane == 31) {
-        s_cnt[0][warp] = ia;
-        s_cnt[1][warp] = ie;
-    }
+    if (lane == 31) s_cnt[0][warp] = make_uint2(ia, ie);
     __syncthreads();
-    int wa = lane < NWARP ? s_cnt[0][lane] : 0, we = lane < NWARP ? s_cnt[1][lane] : 0;
+    const uint2 per_warp = lane < NWARP ? s_cnt[0][lane] : make_uint2(0u, 0u);
+    int wa = per_warp.x, we = per_warp.y;
     const int ties = a.top - __reduce_add_sync(0xffffffffu, wa);
     wa = __reduce_add_sync(0xffffffffu, lane < warp ? wa : 0);
     we = __reduce_add_sync(0xffffffffu, lane < warp ? we : 0);
