@@ -63,8 +63,7 @@ __global__ void __launch_bounds__(NT) plan_pages_kernel(const PagePlanArgs a) {
     int* s_start = sm;                    // [B + 1] first token
     int* s_len = s_start + a.B + 1;       // [B] tokens held
     int* s_new = s_len + a.B;             // [B] new pages of earlier sequences
-    int* s_back = s_new + a.B;            // [B] returning pages
-    int* s_backx = s_back + a.B;          // [B] returning pages of earlier sequences
+    int* s_backx = s_new + a.B;           // [B] returning pages of earlier sequences
     __shared__ unsigned s_sum[5][32];
     __shared__ int s_total[3];            // tokens, new pages, returning pages
     __shared__ bool s_last;
@@ -151,7 +150,6 @@ __global__ void __launch_bounds__(NT) plan_pages_kernel(const PagePlanArgs a) {
         s_start[b] = at_got;
         s_len[b] = n[e];
         s_new[b] = at_new;
-        s_back[b] = fits ? give : 0;
         s_backx[b] = at_back;
         sum_back += fits ? give : 0;
         at_got += got[e];
@@ -185,17 +183,21 @@ __global__ void __launch_bounds__(NT) plan_pages_kernel(const PagePlanArgs a) {
         while (x >= a.num_pages) x -= a.num_pages;
         return static_cast<int>(x);
     };
+    auto last_at_or_before = [&](const int* from, int x) {   // the last sequence with from[b] <= x
+        int lo = 0, hi = a.B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (from[mid] <= x) lo = mid;
+            else hi = mid - 1;
+        }
+        return lo;
+    };
     for (int b = blockIdx.x * NT + threadIdx.x; b <= a.B; b += gridDim.x * NT) a.token_start[b] = s_start[b];
     // ---- token arrays and new block-table entries
     for (int i = blockIdx.x * NT + threadIdx.x; i < a.max_tokens; i += gridDim.x * NT) {
         int pos = 0, slot = -1;
         if (i < tokens) {
-            int lo = 0, hi = a.B - 1;     // the last sequence that starts at or before i
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (s_start[mid] <= i) lo = mid;
-                else hi = mid - 1;
-            }
+            const int lo = last_at_or_before(s_start, i);
             pos = s_len[lo] + (i - s_start[lo]);
             const int blk = pos >> a.page_shift;
             const int k = blk - ((s_len[lo] + ps - 1) >> a.page_shift);
@@ -207,12 +209,10 @@ __global__ void __launch_bounds__(NT) plan_pages_kernel(const PagePlanArgs a) {
         a.slot_map[i] = slot;
         a.position[i] = pos;
     }
-    // ---- pages that return, a warp per sequence
-    const int lane = threadIdx.x & 31;
-    for (int b = blockIdx.x * (NT / 32) + (threadIdx.x >> 5); b < a.B; b += gridDim.x * (NT / 32)) {
-        const int give = s_back[b];
-        for (int i = lane; i < give; i += 32)
-            a.ring[ring_at(count + s_backx[b] + i)] = a.table[static_cast<size_t>(b) * a.max_blocks + i];
+    // ---- pages that return, dealt evenly over the grid
+    for (int r = blockIdx.x * NT + threadIdx.x; r < s_total[2]; r += gridDim.x * NT) {
+        const int b = last_at_or_before(s_backx, r);
+        a.ring[ring_at(count + r)] = a.table[static_cast<size_t>(b) * a.max_blocks + (r - s_backx[b])];
     }
 }
 
@@ -223,10 +223,10 @@ static cudaError_t launch(const PagePlanArgs& a, int blocks, cudaStream_t st) {
     auto kern = plan_pages_kernel<E>;
     static std::atomic<unsigned long long> attr_done{0};
     cudaError_t e = once_per_device(attr_done, [&] {
-        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (5 * NT * E + 1) * 4);
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (4 * NT * E + 1) * 4);
     });
     if (e != cudaSuccess) return e;
-    return launch_kernel(kern, dim3(blocks), dim3(NT), (5 * a.B + 1) * 4, st, true, a);
+    return launch_kernel(kern, dim3(blocks), dim3(NT), (4 * a.B + 1) * 4, st, true, a);
 }
 
 cudaError_t launch_plan_pages(const PagePlanArgs& a, int sms, cudaStream_t st) {

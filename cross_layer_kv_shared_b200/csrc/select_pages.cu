@@ -288,10 +288,10 @@ cudaError_t launch(const PagedSelectArgs& args, int sms, cudaStream_t st) {
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, NT * E * 4);
     });
     if (e != cudaSuccess) return e;
-    // CTAs per (sequence, kv head): as many as the multiprocessors allow and the blocks can use
+    // CTAs per (sequence, kv head): as many as fit at two CTAs per SM and the blocks can use
     const int units = a.B * a.Hkv;
     a.cluster = 1;
-    while (a.cluster < MAX_CLUSTER && units * a.cluster * 2 <= sms && a.cluster * NWARP * 16 < a.max_blocks) a.cluster *= 2;
+    while (a.cluster < MAX_CLUSTER && units * a.cluster * 2 <= 2 * sms && a.cluster * NWARP * 16 < a.max_blocks) a.cluster *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(units * a.cluster);
     cfg.blockDim = dim3(NT);
