@@ -251,18 +251,24 @@ def kvshare_append_lowrank(h, cache: Cache, k_new, v_new, score, pos, stream=Non
 # ---- paged cache. A pool's sizes are not known to the C side, so these entry points check
 # their tensors' shapes, types and strides here (EINVAL) before the call; that the memory is
 # the context's device's is checked there.
-_TYPES = {}     # torch type -> kvshare_dtype, filled with the first Pages
+_torch = None   # torch, imported with the first tensor
+
+
+def _use_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
 
 
 def _dense(t, dtype, shape) -> bool:
     return t.dtype is dtype and t.shape == shape and t.is_contiguous()
 
 
-def _device_stream(stream, t) -> Optional[int]:
-    """The given stream, or torch's current one on the tensor's own device."""
+def _device_stream(stream, device: int) -> Optional[int]:
+    """The given stream, or torch's current one on the tensors' own device."""
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
+        return _torch._C._cuda_getCurrentRawStream(device)
     return int(getattr(stream, "cuda_stream", stream))
 
 
@@ -283,10 +289,10 @@ class Pages:
     bound_scale: object = None
 
     def __post_init__(self):
-        import torch
-        _TYPES.update({torch.bfloat16: KVS_BF16, torch.float32: KVS_F32})
+        torch = _torch or _use_torch()
+        types = {torch.bfloat16: KVS_BF16, torch.float32: KVS_F32}
         k, t = self.k, self.block_table
-        ok = k.dtype in _TYPES and k.dim() == 5 and t.dim() == 2
+        ok = k.dtype in types and k.dim() == 5 and t.dim() == 2
         ok = ok and _dense(k, k.dtype, k.shape) and _dense(self.v, k.dtype, k.shape) and \
             _dense(t, torch.int32, t.shape) and _dense(self.lengths, torch.int32, (t.shape[0],))
         if self.bound_codes is not None or self.bound_scale is not None:
@@ -302,7 +308,9 @@ class Pages:
         keep("_c", c)
         keep("_ref", ctypes.byref(c))
         # what a context must have been created with
-        keep("_model", (k.shape[2], k.shape[4], _TYPES[k.dtype]))
+        keep("_model", (k.shape[2], k.shape[4], types[k.dtype]))
+        keep("_dtype", k.dtype)
+        keep("_device", k.get_device())
 
 
 def _layer_range(pages: Pages, cfg, q, l1):
@@ -310,84 +318,81 @@ def _layer_range(pages: Pages, cfg, q, l1):
     L = q.shape[0] if q.dim() == 4 else 0
     l1 = L if l1 is None else int(l1)
     shape = (L, pages._c.batch, cfg[0], cfg[1][1])
-    return (shape, l1) if 0 <= l1 <= L and _dense(q, pages.k.dtype, shape) else None
+    return (shape, l1) if 0 <= l1 <= L and _dense(q, pages._dtype, shape) else None
 
 
 def kvshare_plan_pages(h, lengths, new_tokens, block_table, ring, ring_state, lengths_out, ring_state_out,
                        token_start, slot_map, position, page_size: int, stream=None, check: bool = True) -> int:
-    from torch import int32
-    st = KVS_EINVAL
-    if block_table.dim() == 2 and ring.dim() == 1 and slot_map.dim() == 1:
-        (B, P), N, M = block_table.shape, ring.shape[0], slot_map.shape[0]
-        if _dense(block_table, int32, (B, P)) and _dense(ring, int32, (N,)) and _dense(slot_map, int32, (M,)) and \
-                _dense(position, int32, (M,)) and _dense(lengths, int32, (B,)) and _dense(new_tokens, int32, (B,)) and \
-                _dense(lengths_out, int32, (B,)) and _dense(ring_state, int32, (2,)) and \
-                _dense(ring_state_out, int32, (2,)) and _dense(token_start, int32, (B + 1,)) and lengths.is_cuda:
-            st = _lib.kvshare_plan_pages(
-                h, lengths.data_ptr(), new_tokens.data_ptr(), block_table.data_ptr(), ring.data_ptr(),
-                ring_state.data_ptr(), lengths_out.data_ptr(), ring_state_out.data_ptr(), token_start.data_ptr(),
-                slot_map.data_ptr(), position.data_ptr(), B, P, page_size, N, M, _device_stream(stream, lengths))
-    if check:
-        _check(st, "kvshare_plan_pages")
+    """Sizes are the tensors': batch and max_blocks of block_table, num_pages of ring, max_tokens of slot_map."""
+    int32, st = (_torch or _use_torch()).int32, KVS_EINVAL
+    if block_table.dim() == 2:
+        (B, P), N, M = block_table.shape, ring.numel(), slot_map.numel()
+        for t, n in ((lengths, B), (new_tokens, B), (block_table, B * P), (ring, N), (ring_state, 2), (lengths_out, B),
+                     (ring_state_out, 2), (token_start, B + 1), (slot_map, M), (position, M)):
+            if t.dtype is not int32 or t.numel() != n or not t.is_contiguous():
+                break
+        else:
+            if lengths.is_cuda:
+                st = _lib.kvshare_plan_pages(
+                    h, lengths.data_ptr(), new_tokens.data_ptr(), block_table.data_ptr(), ring.data_ptr(),
+                    ring_state.data_ptr(), lengths_out.data_ptr(), ring_state_out.data_ptr(), token_start.data_ptr(),
+                    slot_map.data_ptr(), position.data_ptr(), B, P, page_size, N, M,
+                    _device_stream(stream, lengths.get_device()))
+    if check and st != KVS_OK:
+        raise KVShareError(st, "kvshare_plan_pages")
     return st
 
 
 def kvshare_append_paged(h, pages: Pages, slot: int, k_new, v_new, slot_map, stream=None, check: bool = True) -> int:
     """k_new, v_new: [tokens][Hkv][d], each token's heads dense; the tokens may be rows of a wider tensor."""
-    from torch import int32
-    st, cfg = KVS_EINVAL, _configs.get(h.value)
-    if cfg is not None and cfg[1] == pages._model and slot_map.dim() == 1:
-        n, (H, d, _) = slot_map.shape[0], pages._model
-        dt, shape = pages.k.dtype, (n, H, d)
-        if _dense(slot_map, int32, (n,)) and k_new.dtype is dt and v_new.dtype is dt and k_new.shape == shape and \
-                v_new.shape == shape:
+    st, cfg, model = KVS_EINVAL, _configs.get(h.value), pages._model
+    if cfg is not None and cfg[1] == model:
+        n, H, d = slot_map.numel(), model[0], model[1]
+        dt, shape = pages._dtype, (n, H, d)
+        if slot_map.dtype is _torch.int32 and slot_map.is_contiguous() and k_new.dtype is dt and v_new.dtype is dt and \
+                k_new.shape == shape and v_new.shape == shape:
             (kr, kh, ke), (vr, vh, ve) = k_new.stride(), v_new.stride()
             if ke == 1 and ve == 1 and (H == 1 or (kh == d and vh == d)):
                 if n <= 1:                      # one token's stride says nothing about its row
                     kr = vr = H * d
                 st = _lib.kvshare_append_paged(h, pages._ref, slot, k_new.data_ptr(), v_new.data_ptr(), kr, vr,
-                                               slot_map.data_ptr(), n, _device_stream(stream, pages.k))
-    if check:
-        _check(st, "kvshare_append_paged")
+                                               slot_map.data_ptr(), n, _device_stream(stream, pages._device))
+    if check and st != KVS_OK:
+        raise KVShareError(st, "kvshare_append_paged")
     return st
 
 
 def kvshare_decode_paged(h, pages: Pages, q, out, lse=None, l0: int = 0, l1: int = None, selected=None, stream=None,
                          check: bool = True) -> int:
-    from torch import float32, int32
     st, cfg = KVS_EINVAL, _configs.get(h.value)
     got = _layer_range(pages, cfg, q, l1) if cfg is not None and cfg[1] == pages._model else None
     if got is not None:
-        shape, l1 = got
+        (shape, l1), float32, top, sp = got, _torch.float32, 0, None
         ok = _dense(out, float32, shape) and (lse is None or _dense(lse, float32, shape[:3]))
-        top = 0
         if selected is not None:
             # an empty list has no address, which would ask for every block
-            top = selected.shape[-1]
-            ok = ok and top > 0 and _dense(selected, int32, (*shape[:2], pages._model[0], top))
+            top, sp = selected.shape[-1], selected.data_ptr()
+            ok = ok and top > 0 and _dense(selected, _torch.int32, (shape[0], shape[1], pages._model[0], top))
         if ok:
             st = _lib.kvshare_decode_paged(h, pages._ref, q.data_ptr(), out.data_ptr(),
-                                           None if lse is None else lse.data_ptr(),
-                                           None if selected is None else selected.data_ptr(), top, l0, l1,
-                                           _device_stream(stream, pages.k))
-    if check:
-        _check(st, "kvshare_decode_paged")
+                                           None if lse is None else lse.data_ptr(), sp, top, l0, l1,
+                                           _device_stream(stream, pages._device))
+    if check and st != KVS_OK:
+        raise KVShareError(st, "kvshare_decode_paged")
     return st
 
 
 def kvshare_select_pages(h, pages: Pages, q, selected, first: int = 1, last: int = 1, l0: int = 0, l1: int = None,
                          stream=None, check: bool = True) -> int:
-    from torch import int32
     st, cfg = KVS_EINVAL, _configs.get(h.value)
     got = _layer_range(pages, cfg, q, l1) if cfg is not None and cfg[1] == pages._model else None
     if got is not None:
-        shape, l1 = got
-        top = selected.shape[-1]
-        if _dense(selected, int32, (*shape[:2], pages._model[0], top)):
+        (shape, l1), top = got, selected.shape[-1]
+        if _dense(selected, _torch.int32, (shape[0], shape[1], pages._model[0], top)):
             st = _lib.kvshare_select_pages(h, pages._ref, q.data_ptr(), selected.data_ptr(), top, first, last, l0, l1,
-                                           _device_stream(stream, pages.k))
-    if check:
-        _check(st, "kvshare_select_pages")
+                                           _device_stream(stream, pages._device))
+    if check and st != KVS_OK:
+        raise KVShareError(st, "kvshare_select_pages")
     return st
 
 
