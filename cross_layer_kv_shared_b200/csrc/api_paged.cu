@@ -11,6 +11,7 @@ using namespace kvs;
 namespace {
 
 constexpr long long INT_LIMIT = 1LL << 31;
+constexpr long long TOKEN_LIMIT = 1LL << 30;   // tokens of a sequence or of one call, counted in int with room to round up
 
 // Makes the context's device current for a call and the caller's current again after it.
 struct DeviceScope {
@@ -58,7 +59,7 @@ kvshare_status check_tables(const kvshare_ctx* c, const kvshare_pages* p) {
     if (p->batch < 1 || p->batch > c->cfg.max_batch || p->max_blocks < 1) return KVS_EINVAL;
     if ((static_cast<long long>(p->max_blocks) - 1) * p->page_size >= c->cfg.max_context) return KVS_EINVAL;
     // tokens of a sequence, and 16-token tiles of the batch, counted in 32 bits
-    if (static_cast<long long>(p->max_blocks) * p->page_size >= INT_LIMIT) return KVS_EINVAL;
+    if (static_cast<long long>(p->max_blocks) * p->page_size > TOKEN_LIMIT) return KVS_EINVAL;
     if (static_cast<long long>(p->batch) * p->max_blocks * (p->page_size / 16) >= INT_LIMIT / c->cfg.num_kv_heads)
         return KVS_EUNSUPPORTED;
     if (!on_device(c, p->block_table, 4) || !on_device(c, p->lengths, 4)) return KVS_EINVAL;
@@ -108,7 +109,7 @@ kvshare_status kvshare_plan_pages(kvshare_t ctx, const int* lengths, const int* 
     const int shift = page_shift(page_size);
     if (batch < 1 || max_blocks < 1 || shift < 0 || num_pages < 1 || max_tokens < 1) return KVS_EINVAL;
     if (static_cast<long long>(batch) * max_blocks >= INT_LIMIT ||
-        static_cast<long long>(max_blocks) * page_size >= INT_LIMIT ||
+        static_cast<long long>(max_blocks) * page_size > TOKEN_LIMIT || max_tokens > TOKEN_LIMIT ||
         static_cast<long long>(num_pages) * page_size >= INT_LIMIT)
         return KVS_EINVAL;
     if (batch > PLAN_MAX_BATCH) return KVS_EUNSUPPORTED;
@@ -149,7 +150,7 @@ kvshare_status kvshare_append_paged(kvshare_t ctx, const kvshare_pages* pages, i
     kvshare_status s = check_pool(ctx, pages);
     if (s != KVS_OK) return s;
     const kvshare_config& cf = ctx->cfg;
-    if (slot < 0 || slot >= pages->slots || tokens < 0) return KVS_EINVAL;
+    if (slot < 0 || slot >= pages->slots || tokens < 0 || tokens > TOKEN_LIMIT) return KVS_EINVAL;
     if (tokens == 0) return KVS_OK;
     const long long es = static_cast<long long>(elem_size(cf.dtype)), row = static_cast<long long>(cf.num_kv_heads) * cf.head_dim;
     if (k_stride < row || v_stride < row || (k_stride * es) % 16 != 0 || (v_stride * es) % 16 != 0) return KVS_EINVAL;
@@ -236,6 +237,8 @@ kvshare_status kvshare_decode_paged(kvshare_t ctx, const kvshare_pages* pages, c
         a.err = ctx->err;
         a.wait_limit = ctx->wait_limit;
         a.ctas = ctx->sms;
+        a.stall_limit = ctx->stall_next ? ctx->stall_limit : 0;
+        ctx->stall_next = 0;
         const cudaStream_t st = static_cast<cudaStream_t>(stream);
         const cudaError_t err = f32 ? launch_decode_paged_f32(D, mix, tmK, tmV, a, st)
                                     : launch_decode_paged_bf16(D, mix, tmK, tmV, a, st);

@@ -105,7 +105,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     constexpr int TILE_BYTES = SUBS * TT * 128;
     extern __shared__ uint8_t smem_dyn[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
-    __shared__ __align__(8) uint64_t bars[NW * NSW];
+    __shared__ __align__(8) uint64_t bars[NW * NSW + 1];
     __shared__ int s_lim[NW * NSW * BLK];
     __shared__ PagedState s_state[NW * 2];
     __shared__ float2 s_ml[NW * 2][NH];          // max and sum of every head of a state
@@ -121,7 +121,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     if (threadIdx.x == 0) {
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
-        for (int i = 0; i < NW * NSW; ++i) mbar_init(&bars[i], 1);
+        for (int i = 0; i < NW * NSW + 1; ++i) mbar_init(&bars[i], 1);
         mbar_init_fence();
     }
     if (threadIdx.x < NW * 2) s_state[threadIdx.x].head0 = -1;
@@ -285,6 +285,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     };
     for (int k = 0; k < min(NSW, my_n); ++k) issue(k);
 
+    if (a.stall_limit > 0 && threadIdx.x == 0) mbar_wait_bounded(&bars[NW * NSW], 0, a.stall_limit, a.err);
     // ---- sequences without tokens: zero output, lse -inf
     for (int b = cta; b < a.B; b += gridDim.x) {
         if (a.lens[b] > 0) continue;

@@ -33,6 +33,7 @@ struct PagedDecodeArgs {
     long long wait_limit;
     int ctas;               // grid: at most one CTA per SM
     int aligned;            // one CTA per unit (set by the launcher)
+    long long stall_limit;  // test hook: > 0: one thread waits that long on a barrier nothing arrives on
 };
 // rows of the K/V tensor-map boxes (tokens per copy)
 int decode_paged_box_rows(bool f32, int d, bool mix, int page_size);

@@ -137,8 +137,8 @@ typedef struct {
  * page_size] is clamped, a page outside [0, num_pages) reads as zeros and is never written,
  * and either makes the next kvshare_sync_status return KVS_EINVAL. Block-table entries past
  * a sequence's last block are not read. Tokens past its length may hold anything (NaN).
- * num_pages * page_size and slots * num_pages * Hkv must stay below 2^31; byte offsets are
- * 64-bit. batch <= max_batch and (max_blocks - 1) * page_size < max_context of the context. */
+ * num_pages * page_size and slots * num_pages * Hkv must stay below 2^31 and max_blocks *
+ * page_size at most 2^30; byte offsets are 64-bit. batch <= max_batch and (max_blocks - 1) * page_size < max_context of the context. */
 typedef struct {
     const void* k;             /* [slots][num_pages][Hkv][page_size][d] dtype of the config   */
     const void* v;
@@ -320,8 +320,8 @@ kvshare_status kvshare_append_lowrank(kvshare_t ctx, const kvshare_cache* cache,
  * page_size takes nothing, and more returning pages than the pool has room for are
  * dropped; both report KVS_EINVAL. lengths_out may be lengths and ring_state_out
  * ring_state; no other two arrays may overlap. A page belongs to one sequence at a time.
- * batch <= 4096 (KVS_EUNSUPPORTED above), batch * max_blocks and max_blocks * page_size
- * below 2^31. */
+ * batch <= 4096 (KVS_EUNSUPPORTED above); batch * max_blocks and num_pages * page_size below
+ * 2^31, max_blocks * page_size and max_tokens at most 2^30. */
 kvshare_status kvshare_plan_pages(kvshare_t ctx, const int* lengths, const int* new_tokens, int* block_table,
                                   int* ring, const int* ring_state, int* lengths_out, int* ring_state_out,
                                   int* token_start, int* slot_map, int* position, int batch, int max_blocks,

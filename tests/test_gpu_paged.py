@@ -590,6 +590,66 @@ def test_two_contexts_on_two_streams(K):
             K.kvshare_destroy(h)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_wait_that_runs_out_is_reported_and_the_context_works_on(K, dtype):
+    torch = torch_mod()
+    pool = Pool(K, dtype, 1, 2, 16, 64, [300, 40], seed=1)
+    h = make(K, dtype, [(K.KVS_SRC_SINGLE, 0, 0)], 4, 2, 64, 2, 304)
+    try:
+        q = queries(pool, 1, 4, seed=1)
+        out, lse = outputs(q)
+        K.kvshare_debug_stall_next(h, True)
+        K.kvshare_decode_paged(h, pool.pages(), q, out, lse)
+        assert K.kvshare_sync_status(h) == K.KVS_ETIMEOUT
+        again, alse = outputs(q)
+        K.kvshare_decode_paged(h, pool.pages(), q, again, alse)
+        assert K.kvshare_sync_status(h) == K.KVS_OK
+        assert torch.equal(out, again) and torch.equal(lse, alse)              # only the spare barrier was waited on
+    finally:
+        K.kvshare_destroy(h)
+
+
+def test_sizes_past_the_counters_are_refused(K):
+    import ctypes
+    torch = torch_mod()
+    pool = Pool(K, "bf16", 1, 2, 16, 64, [40, 3], seed=1)
+    h = make(K, "bf16", [(K.KVS_SRC_SINGLE, 0, 0)], 4, 2, 64, 2, 48)
+    try:
+        lib, p = K._lib, pool.pages()
+        q = queries(pool, 1, 4, seed=1)
+        out, lse = outputs(q)
+        sel = torch.zeros(64, dtype=torch.int32, device="cuda")
+        n0 = K.kvshare_launch_count(h)
+
+        def call(f, **kw):
+            c = K.kvshare_pages.from_buffer_copy(p._c)
+            for k, x in kw.items():
+                setattr(c, k, x)
+            r = ctypes.byref(c)
+            if f == "decode":
+                return lib.kvshare_decode_paged(h, r, q.data_ptr(), out.data_ptr(), lse.data_ptr(), None, 0, 0, 1, None)
+            if f == "append":
+                return lib.kvshare_append_paged(h, r, 0, q.data_ptr(), q.data_ptr(), 128, 128, sel.data_ptr(), 1, None)
+            return lib.kvshare_select_pages(h, r, q.data_ptr(), sel.data_ptr(), 4, 1, 1, 0, 1, None)
+        for f in ("decode", "append", "select"):
+            for kw in (dict(page_size=24), dict(page_size=8), dict(page_size=512), dict(num_pages=0), dict(slots=0),
+                       dict(num_pages=1 << 27), dict(slots=1 << 30), dict(k=None), dict(v=p._c.v + 2)):
+                assert call(f, **kw) == K.KVS_EINVAL, (f, kw)
+        for f in ("decode", "select"):
+            for kw in (dict(batch=0), dict(batch=3), dict(max_blocks=0), dict(max_blocks=4), dict(max_blocks=1 << 27),
+                       dict(block_table=None), dict(lengths=p._c.lengths + 1)):
+                assert call(f, **kw) == K.KVS_EINVAL, (f, kw)
+        i = sel.data_ptr()
+        plan = lambda B=2, P=2, ps=16, N=4, M=4: lib.kvshare_plan_pages(h, *[i] * 10, B, P, ps, N, M, None)  # noqa: E731
+        for kw in (dict(B=0), dict(P=0), dict(ps=17), dict(N=0), dict(M=0), dict(P=1 << 27), dict(N=1 << 27),
+                   dict(M=(1 << 30) + 1)):
+            assert plan(**kw) == K.KVS_EINVAL, kw
+        assert plan(B=4097) == K.KVS_EUNSUPPORTED
+        assert K.kvshare_launch_count(h) == n0 and K.kvshare_sync_status(h) == K.KVS_OK
+    finally:
+        K.kvshare_destroy(h)
+
+
 # ------------------------------------------------------------------------------- refusals
 def test_refusals_launch_nothing(K):
     torch = torch_mod()
