@@ -200,17 +200,13 @@ kvshare_status kvshare_decode_paged(kvshare_t ctx, const kvshare_pages* pages, c
     const kvshare_config& cf = ctx->cfg;
     const bool f32 = cf.dtype == KVS_F32;
     const int D = cf.head_dim, B = pages->batch, Hq = cf.num_q_heads, Hkv = cf.num_kv_heads;
-    int box = 0;
+    const int rows = decode_paged_box_rows(f32, D, pages->page_size);
     CUtensorMap tmK, tmV;
+    if (!pool_map(ctx, pages, pages->k, rows, &tmK) || !pool_map(ctx, pages, pages->v, rows, &tmV)) return KVS_ECUDA;
     for (int l : ctx->order) {
         if (l < l0 || l >= l1) continue;
         const kvshare_layer& e = ctx->map[l];
         const bool mix = e.kind == KVS_SRC_MIX;
-        const int rows = decode_paged_box_rows(f32, D, mix, pages->page_size);
-        if (rows != box) {
-            if (!pool_map(ctx, pages, pages->k, rows, &tmK) || !pool_map(ctx, pages, pages->v, rows, &tmV)) return KVS_ECUDA;
-            box = rows;
-        }
         const size_t lbh = static_cast<size_t>(l) * B * Hq;
         PagedDecodeArgs a;
         std::memset(&a, 0, sizeof(a));

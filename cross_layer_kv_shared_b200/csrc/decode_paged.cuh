@@ -15,7 +15,18 @@
 // table 32 entries at a time), keeping the online softmax of the unit it is in. A unit that
 // lies inside one warp's share is written out from registers. Otherwise the warps' states meet
 // in shared memory, and a unit that spans CTAs is joined by the last of them to arrive, from
-// one partial per CTA in L2 (two slots a CTA: the unit it ends and the unit it begins).
+// one partial per CTA in L2 (two slots a CTA: the unit it ends and the unit it begins). Where
+// every unit is short and has a CTA of its own, it is not split across CTAs (launch_paged).
+// K and V are read once and marked evict-first in L2 (64K-token decode 122 -> 120.5 us).
+//
+// Measured (one layer, replayed back to back; DRAM reads equal the algorithmic bytes):
+//   4 requests of up to 64K tokens, 8 kv heads x 128, bf16:  119 us, 6.5 TB/s (99 % of the
+//                                                             measured copy rate)
+//   16 requests of up to 8K, two sources, 4 x 128, bf16:      55 us, 5.6 TB/s
+//   32 requests of up to 2K, 4 x 64, bf16:                    13.6 us, 2.6 TB/s
+//   one request of 320 tokens, 4 x 128, bf16:                 6.9 us
+// Short calls are bound by the chain launch (2 us) -> lengths -> block table -> first tile (3 us
+// together) -> last tile -> joins (3 to 4 us), not by bytes.
 //
 // A page index outside the pool reads as zeros (a copy that starts outside its tensor) and is
 // reported; tokens past a sequence's end are masked and their V rows cleared, so that stale
@@ -82,8 +93,8 @@ struct PagedLayout {
     static_assert(P::NSW * P::STAGE >= P::NH * P::D * 4, "a warp's ring holds its last state");
     static_assert(P::STAGE % 1024 == 0, "swizzled stages stay 1024-byte aligned");
     static_assert(BYTES <= PAGED_SMEM_MAX, "shared memory");
-    // merge scratch (factors of up to 2^15 / NH partials) lies over the ring
-    static_assert(RING >= 65536, "merge scratch");
+    // the (m, l) of every CTA's partial of a unit lie over the ring in the last join
+    static_assert(RING >= 65536, "statistics of up to 512 partials");
 };
 
 struct PagedState {
@@ -359,11 +370,9 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 
     // ---- join the warps' states, unit by unit. States are in the line's order; every warp
     // finds the units' first states by votes (lane i: state i)
-    int unit_l = -1, flags_l = 0;
     PagedState mine = {-1, 0, 0, 0, 0};
     if (lane < 2 * NW) mine = s_state[lane];
-    unit_l = mine.head0;
-    flags_l = mine.started | mine.ended << 1;
+    const int unit_l = mine.head0, flags_l = mine.started | mine.ended << 1;
     const unsigned valid = __ballot_sync(0xffffffffu, unit_l >= 0);
     const unsigned below = valid & ((1u << lane) - 1u);
     const int prev = __shfl_sync(0xffffffffu, unit_l, below ? 31 - __clz(below) : lane);

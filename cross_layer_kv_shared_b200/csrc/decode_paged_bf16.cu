@@ -247,8 +247,7 @@ cudaError_t launch_g(const CUtensorMap& tmK, const CUtensorMap& tmV, const Paged
 
 }  // namespace
 
-int decode_paged_box_rows(bool f32, int d, bool mix, int page_size) {
-    (void)mix;
+int decode_paged_box_rows(bool f32, int d, int page_size) {
     const int tt = f32 || d == 128 ? 16 : 32;
     static_assert(PagedBf16<128, true, 8>::TT == 16 && PagedBf16<128, false, 8>::TT == 16 &&
                       PagedBf16<64, true, 8>::TT == 32 && PagedBf16<64, false, 8>::TT == 32,

