@@ -84,6 +84,8 @@ __global__ void __launch_bounds__(NT) select_pages_kernel(const PagedSelectArgs 
     const int C = a.cluster, rank = C > 1 ? static_cast<int>(cluster_rank()) : 0;
     const int unit = blockIdx.x / C, b = unit / a.Hkv, j = unit - b * a.Hkv;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // CTA 0 must run before its memory is written to: arrive now, wait where that begins
+    if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     grid_dep_wait();
     if (threadIdx.x == 0) grid_dep_launch();
     // the first step's pages and this warp's query are on their way beside the length
@@ -110,6 +112,7 @@ __global__ void __launch_bounds__(NT) select_pages_kernel(const PagedSelectArgs 
     if (held <= a.top) {                            // every block, whatever its score (the whole cluster)
         if (rank == 0)
             for (int i = threadIdx.x; i < a.top; i += NT) out[i] = i < held ? i : -1;
+        if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
         return;
     }
     // ---- the group's query codes, positive part then negative part
@@ -127,8 +130,8 @@ __global__ void __launch_bounds__(NT) select_pages_kernel(const PagedSelectArgs 
         }
         if (lane == 0) s_scale[warp] = s;
     }
-    if (C > 1) cluster_sync();                      // also: CTA 0 runs before its memory is written to
-    else __syncthreads();
+    __syncthreads();
+    if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     // ---- scores: 16 pages a warp and step, dealt over the cluster
     const uint32_t keys0 = C > 1 ? in_first_cta(s_key) : smem_u32(s_key);
     const int begin = (rank * NWARP + warp) * 16;
