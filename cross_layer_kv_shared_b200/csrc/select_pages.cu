@@ -19,9 +19,11 @@
 // found bit by bit from the highest bit that differs, a count over the block each, ending as
 // soon as exactly `top` keys are at or above the candidate; the kept blocks are written in
 // ascending order by a prefix sum. Ties go to the lowest block; the first and last blocks asked
-// for are kept whatever their score. Measured: 8 heads x 512 pages 6.5 us, 64 rows x 1024 pages
-// of 128 channels 9.8 us (17 MB of codes), both mostly the chain of dependent steps; with a
-// score kernel and a choosing kernel a sparse step of one request took 19.1 us, now 17.5.
+// for are kept whatever their score. Measured: 8 heads x 512 pages 6.1 us, 64 rows x 1024 pages
+// of 128 channels 7.7 us (17 MB of codes), both mostly the chain of dependent steps; a step's
+// codes are requested before the query codes are made (9.2 -> 7.7 us). Two CTAs on a
+// multiprocessor for twice the cluster: 11.6 us (they do not fit at once), or 9.1 us at 64
+// registers, with spills.
 #include "kvs_device.cuh"
 #include "kvs_paged.h"
 
@@ -115,6 +117,31 @@ __global__ void __launch_bounds__(NT) select_pages_kernel(const PagedSelectArgs 
         if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
         return;
     }
+    // ---- a step's codes and scales: pages p0 + r and + 8, from each source
+    constexpr int NS = MIX ? 2 : 1;
+    const int begin = (rank * NWARP + warp) * 16;
+    uint4 x[NS][2][PIECES];
+    float sp[NS][2];
+    auto load = [&](int p0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int p = p0 + r + 8 * i;
+            int page = p >= held ? -1 : p0 == begin ? first_page[i] : table[p];
+            if (p < held && (page < 0 || page >= a.num_pages)) {
+                atomicOr(a.err, ERR_RANGE);
+                page = -1;                          // scores as a page of zeros
+            }
+#pragma unroll
+            for (int src = 0; src < NS; ++src) {
+                const size_t row = (static_cast<size_t>(src == 0 ? a.src0 : a.src1) * a.num_pages + max(page, 0)) * a.Hkv + j;
+                const uint4* at = reinterpret_cast<const uint4*>(a.codes + row * 2 * D) + c4;
+                sp[src][i] = page >= 0 ? a.scales[row] : 0.f;
+#pragma unroll
+                for (int k = 0; k < PIECES; ++k) x[src][i][k] = page >= 0 ? __ldg(at + 4 * k) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+    };
+    if (begin < held) load(begin);
     // ---- the group's query codes, positive part then negative part
     static_assert(NH <= NWARP, "a warp per head");
     if (warp < NH) {
@@ -134,32 +161,10 @@ __global__ void __launch_bounds__(NT) select_pages_kernel(const PagedSelectArgs 
     if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     // ---- scores: 16 pages a warp and step, dealt over the cluster
     const uint32_t keys0 = C > 1 ? in_first_cta(s_key) : smem_u32(s_key);
-    const int begin = (rank * NWARP + warp) * 16;
-    for (int p0 = begin; p0 < held; p0 += C * NWARP * 16) {
-        int page[2];
+    for (int p0 = begin; p0 < held;) {
         float score[NB][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {               // pages p0 + r and + 8
-            const int p = p0 + r + 8 * i;
-            page[i] = p >= held ? -1 : p0 == begin ? first_page[i] : table[p];
-            if (p < held && (page[i] < 0 || page[i] >= a.num_pages)) {
-                atomicOr(a.err, ERR_RANGE);
-                page[i] = -1;                       // scores as a page of zeros
-            }
-        }
-#pragma unroll
-        for (int src = 0; src < (MIX ? 2 : 1); ++src) {
-            const size_t slot = static_cast<size_t>(src == 0 ? a.src0 : a.src1) * a.num_pages;
-            uint4 x[2][PIECES];
-            float sp[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const size_t row = (slot + max(page[i], 0)) * a.Hkv + j;
-                const uint4* at = reinterpret_cast<const uint4*>(a.codes + row * 2 * D) + c4;
-                sp[i] = page[i] >= 0 ? a.scales[row] : 0.f;
-#pragma unroll
-                for (int k = 0; k < PIECES; ++k) x[i][k] = page[i] >= 0 ? __ldg(at + 4 * k) : make_uint4(0u, 0u, 0u, 0u);
-            }
+        for (int src = 0; src < NS; ++src) {
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
                 int acc[4] = {0, 0, 0, 0};
@@ -167,14 +172,14 @@ __global__ void __launch_bounds__(NT) select_pages_kernel(const PagedSelectArgs 
 #pragma unroll
                 for (int k = 0; k < PIECES; ++k) {
                     const uint4 q = qc[4 * k];
-                    const uint32_t a0[4] = {x[0][k].x, x[1][k].x, x[0][k].y, x[1][k].y};
-                    const uint32_t a1[4] = {x[0][k].z, x[1][k].z, x[0][k].w, x[1][k].w};
+                    const uint32_t a0[4] = {x[src][0][k].x, x[src][1][k].x, x[src][0][k].y, x[src][1][k].y};
+                    const uint32_t a1[4] = {x[src][0][k].z, x[src][1][k].z, x[src][0][k].w, x[src][1][k].w};
                     mma_s8(acc, a0, q.x, q.y);
                     mma_s8(acc, a1, q.z, q.w);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float s = __fmul_rn(__fmul_rn(static_cast<float>(acc[i]), s_scale[nb * 8 + 2 * c4 + (i & 1)]), sp[i >> 1]);
+                    const float s = __fmul_rn(__fmul_rn(static_cast<float>(acc[i]), s_scale[nb * 8 + 2 * c4 + (i & 1)]), sp[src][i >> 1]);
                     if (!MIX) {
                         score[nb][i] = s;
                     } else {
@@ -184,6 +189,9 @@ __global__ void __launch_bounds__(NT) select_pages_kernel(const PagedSelectArgs 
                 }
             }
         }
+        const int done = p0;
+        p0 += C * NWARP * 16;
+        if (p0 < held) load(p0);                    // on its way while this step's scores are placed
 #pragma unroll
         for (int i = 0; i < 2; ++i) {               // the group's largest score of each page
             float top = NEG_INF;
@@ -194,7 +202,7 @@ __global__ void __launch_bounds__(NT) select_pages_kernel(const PagedSelectArgs 
                     if (nb * 8 + 2 * c4 + k < a.g) top = fmaxf(top, score[nb][2 * i + k]);
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int p = p0 + r + 8 * i;
+            const int p = done + r + 8 * i;
             if (c4 == 0 && p < held) {
                 const uint32_t key = p < a.first || p >= held - a.last ? 0xffffffffu : score_key(top);
                 asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(keys0 + 4u * p), "r"(key) : "memory");
@@ -293,10 +301,10 @@ cudaError_t launch(const PagedSelectArgs& args, int sms, cudaStream_t st) {
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, NT * E * 4);
     });
     if (e != cudaSuccess) return e;
-    // CTAs per (sequence, kv head): as many as fit at two CTAs per SM and the blocks can use
+    // CTAs per (sequence, kv head): as many as have a multiprocessor each and the blocks can use
     const int units = a.B * a.Hkv;
     a.cluster = 1;
-    while (a.cluster < MAX_CLUSTER && units * a.cluster * 2 <= 2 * sms && a.cluster * NWARP * 16 < a.max_blocks) a.cluster *= 2;
+    while (a.cluster < MAX_CLUSTER && units * a.cluster * 2 <= sms && a.cluster * NWARP * 16 < a.max_blocks) a.cluster *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(units * a.cluster);
     cfg.blockDim = dim3(NT);
