@@ -409,44 +409,26 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         for (int c = k / VALS; c > 0; --c) rest &= rest - 1u;
         const int i = __ffs(rest) - 1;
         const unsigned states = states_from(i);
-        // four states at a time, their loads together (missing ones repeat the first with weight 0)
-        auto next4 = [](unsigned& r, int (&q)[4]) {
-            int n = 0;
+        // a warp has at most one state of a unit (even: begun by an earlier warp, in the save area;
+        // odd: over its ring), so the loop over the warps is static and its loads independent
+        float2 M = make_float2(NEG_INF, NEG_INF), mx[NW], my[NW];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                q[x] = r != 0u ? __ffs(r) - 1 : q[0];
-                n += r != 0u ? 1 : 0;
-                r &= r - 1u;
-            }
-            return n;
-        };
-        float2 M = make_float2(NEG_INF, NEG_INF);
-        int q[4];
-        for (unsigned r = states; r != 0u;) {
-            next4(r, q);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                M.x = fmaxf(M.x, s_ml[q[x]][hd.x].x);
-                M.y = fmaxf(M.y, s_ml[q[x]][hd.y].x);
-            }
+        for (int w = 0; w < NW; ++w) {
+            const unsigned own = (states >> (2 * w)) & 3u;
+            mx[w] = s_ml[2 * w + (own >> 1)][hd.x];
+            my[w] = s_ml[2 * w + (own >> 1)][hd.y];
+            if (own == 0u) mx[w] = my[w] = make_float2(NEG_INF, 0.f);     // whatever was there: no state
+            M.x = fmaxf(M.x, mx[w].x);
+            M.y = fmaxf(M.y, my[w].x);
         }
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         float2 l = make_float2(0.f, 0.f);
-        for (unsigned r = states; r != 0u;) {
-            const int n = next4(r, q);
-            float4 v[4];
-            float2 mx[4], my[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                // odd states lie over their warp's ring, even ones in the save area
-                v[x] = reinterpret_cast<const float4*>(
-                    smem + ((q[x] & 1) ? (q[x] >> 1) * NSW * P::STAGE : L::RING + (q[x] >> 1) * VALS * 16))[idx];
-                mx[x] = s_ml[q[x]][hd.x];
-                my[x] = s_ml[q[x]][hd.y];
-            }
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                if (x < n) add_state(acc, l, v[x], mx[x], my[x], M);
+        for (int w = 0; w < NW; ++w) {
+            const unsigned own = (states >> (2 * w)) & 3u;
+            float4 v = reinterpret_cast<const float4*>(smem + (own >= 2u ? w * NSW * P::STAGE : L::RING + w * VALS * 16))[idx];
+            if (own == 0u) v = make_float4(0.f, 0.f, 0.f, 0.f);
+            add_state(acc, l, v, mx[w], my[w], M);
         }
         if ((splits >> i) & 1u) {
             float* part = a.ws + static_cast<size_t>(2 * cta + s_state[i].started) * per;
