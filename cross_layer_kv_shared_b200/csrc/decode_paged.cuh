@@ -23,8 +23,8 @@
 //   4 requests of up to 64K tokens, 8 kv heads x 128, bf16:  119 us, 6.5 TB/s (99 % of the
 //                                                             measured copy rate)
 //   16 requests of up to 8K, two sources, 4 x 128, bf16:      55 us, 5.6 TB/s
-//   32 requests of up to 2K, 4 x 64, bf16:                    13.6 us, 2.6 TB/s
-//   one request of 320 tokens, 4 x 128, bf16:                 6.9 us
+//   32 requests of up to 2K, 4 x 64, bf16:                    13.3 us, 2.7 TB/s
+//   one request of 320 tokens, 4 x 128, bf16:                 6.5 us
 // Short calls are bound by the chain launch (2 us) -> lengths -> block table -> first tile (3 us
 // together) -> last tile -> joins (3 to 4 us), not by bytes.
 //

@@ -5,34 +5,16 @@
 //   softmax of those heads, the weights written to shared memory
 //   output: lane = four channels (at d = 64 the half warps take alternate tokens); the weights
 //           of a token are read as broadcasts
-// 128-byte swizzled tiles keep every 16-byte read of K and V free of bank conflicts. At g = 8
-// the loop takes about half of the fp32 issue slots that a tile's HBM time leaves; larger
-// groups are bound by them.
+// 128-byte swizzled tiles keep every 16-byte read of K and V free of bank conflicts. Groups of up
+// to 4 stream near HBM speed (4 requests of up to 32K tokens, 4 x 128: 64.7 us, 87 % of the
+// measured copy rate); at 8 and 16 the two warps that a scheduler has wait on their own chains
+// of reads and multiply-adds (32 us where HBM needs 14, 8K tokens; 55 us for 7, 4K tokens).
+// Tensor cores with tf32 operands in two parts were hardly faster (30 and 45 us) and lost
+// precision (1.5e-6 against 3e-7); paired multiply-adds gained 4 % and spilled at 16.
 #include "decode_paged.cuh"
 
 namespace kvs {
 namespace {
-
-// Pairs of fp32 in one 64-bit register: one instruction for two multiply-adds (sm_100 on).
-typedef unsigned long long pair_t;
-__device__ __forceinline__ pair_t pack2(float x, float y) {
-    pair_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ float2 unpack2(pair_t v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ void fma2(pair_t& d, pair_t a, pair_t b) {
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
-}
-__device__ __forceinline__ pair_t mul2(pair_t a, pair_t b) {
-    pair_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 
 template <int D_, bool MIX, int NH_>
 struct PagedF32 {
@@ -41,9 +23,7 @@ struct PagedF32 {
     static constexpr int SUBW = 32;
     static constexpr int STAGE = 2 * NSRC * TT * D * 4;
     static constexpr int NW = STAGE <= 8192 || (STAGE <= 16384 && NH <= 8) ? 8 : 4;
-    // queries of the unit, a head's quarters 16 bytes further apart than their length, so that the
-    // four that a warp reads at once lie in different banks
-    static constexpr int QQ = D / 4 + 4, QF = NH * 4 * QQ;
+    static constexpr int QF = NH * D;                     // queries of the unit
     static constexpr int WARP_FLOATS = QF + TT * NH + NH; // + weights [TT][NH] + corrections [NH]
     static constexpr int NSW = paged_stages(NW, STAGE, NH, D, WARP_FLOATS);
     static constexpr int SUB_BYTES = TT * 128, TILE_BYTES = TT * D * 4;
@@ -52,7 +32,7 @@ struct PagedF32 {
     static constexpr int TP = 32 / EL;                    // V rows read at once
     static_assert(NH % 4 == 0, "heads are dealt to the quarters");
 
-    pair_t o[NH][2];       // channels 4 (lane % EL) .. + 3; at TP = 2 the share of this half's tokens
+    float o[NH][4];        // channels 4 (lane % EL) .. + 3; at TP = 2 the share of this half's tokens
     float m[HQ], l[HQ];    // heads quarter * HQ + i
     float w, w1;
     int lane;
@@ -71,10 +51,10 @@ struct PagedF32 {
         const float* qg = static_cast<const float*>(a.q) + (static_cast<size_t>(b) * a.Hq + static_cast<size_t>(j) * a.g) * D;
         __syncwarp();
         for (int i = lane; i < NH * D / 4; i += 32)
-            *reinterpret_cast<float4*>(sq + i / (D / 16) * QQ + i % (D / 16) * 4) = 4 * i < a.g * D ? *reinterpret_cast<const float4*>(qg + 4 * i)
+            *reinterpret_cast<float4*>(sq + 4 * i) = 4 * i < a.g * D ? *reinterpret_cast<const float4*>(qg + 4 * i)
                                                                      : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int h = 0; h < NH; ++h) o[h][0] = o[h][1] = 0ull;
+        for (int h = 0; h < NH; ++h) o[h][0] = o[h][1] = o[h][2] = o[h][3] = 0.f;
 #pragma unroll
         for (int i = 0; i < HQ; ++i) {
             m[i] = NEG_INF;
@@ -85,42 +65,34 @@ struct PagedF32 {
         __syncwarp();
     }
 
-    // acc[r][h] = q_h . row (lane % 8 + 8 r) over this lane's quarter of the channels
+    // acc[r][h] += q_h . row (lane % 8 + 8 r) over this lane's quarter of the channels
     __device__ void dots(const uint8_t* kt, float (&acc)[2][NH]) const {
         const int row = lane & 7, quarter = lane >> 3;
-        pair_t even_odd[2][NH];                           // sums of the even and of the odd channels
-#pragma unroll
-        for (int h = 0; h < NH; ++h) even_odd[0][h] = even_odd[1][h] = 0ull;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
             const int chunk = quarter * (D / 16) + i;     // 16-byte chunk of the row
             const uint32_t off = (chunk >> 3) * SUB_BYTES + swz128(row, chunk & 7);
-            const ulonglong2 k0 = *reinterpret_cast<const ulonglong2*>(kt + off);
-            const ulonglong2 k1 = *reinterpret_cast<const ulonglong2*>(kt + off + 8 * 128);
+            const float4 k0 = *reinterpret_cast<const float4*>(kt + off);
+            const float4 k1 = *reinterpret_cast<const float4*>(kt + off + 8 * 128);
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
-                const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(sq + (h * 4 + quarter) * QQ + i * 4);
-                fma2(even_odd[0][h], q.x, k0.x);
-                fma2(even_odd[1][h], q.x, k1.x);
-                fma2(even_odd[0][h], q.y, k0.y);
-                fma2(even_odd[1][h], q.y, k1.y);
+                const float4 q = *reinterpret_cast<const float4*>(sq + h * D + chunk * 4);
+                acc[0][h] = fmaf(q.w, k0.w, fmaf(q.z, k0.z, fmaf(q.y, k0.y, fmaf(q.x, k0.x, acc[0][h]))));
+                acc[1][h] = fmaf(q.w, k1.w, fmaf(q.z, k1.z, fmaf(q.y, k1.y, fmaf(q.x, k1.x, acc[1][h]))));
             }
         }
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int h = 0; h < NH; ++h) {
-                const float2 x = unpack2(even_odd[r][h]);
-                acc[r][h] = x.x + x.y;
-            }
     }
 
     __device__ void tile(const PagedDecodeArgs& a, const uint8_t* st, int, int, const int* lim, bool cut) {
         const int quarter = lane >> 3;
         float acc[2][NH];
+#pragma unroll
+        for (int h = 0; h < NH; ++h) acc[0][h] = acc[1][h] = 0.f;
         dots(st, acc);
         if (MIX) {
             float acc2[2][NH];
+#pragma unroll
+            for (int h = 0; h < NH; ++h) acc2[0][h] = acc2[1][h] = 0.f;
             dots(st + 2 * TILE_BYTES, acc2);
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
@@ -177,24 +149,22 @@ struct PagedF32 {
         __syncwarp();
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-            const pair_t c = pack2(sc[h], sc[h]);
-            o[h][0] = mul2(o[h][0], c);
-            o[h][1] = mul2(o[h][1], c);
+            const float c = sc[h];
+            o[h][0] *= c;
+            o[h][1] *= c;
+            o[h][2] *= c;
+            o[h][3] *= c;
         }
         const int chunk = lane % EL;
-        const pair_t ww = pack2(w, w), ww1 = pack2(w1, w1);
 #pragma unroll
         for (int i = 0; i < TT / TP; ++i) {
             const int t = i * TP + lane / EL;
             const uint32_t off = (chunk >> 3) * SUB_BYTES + swz128(t, chunk & 7);
-            ulonglong2 v = *reinterpret_cast<const ulonglong2*>(st + TILE_BYTES + off);
+            float4 v = *reinterpret_cast<const float4*>(st + TILE_BYTES + off);
             if (MIX) {
-                const ulonglong2 v2 = *reinterpret_cast<const ulonglong2*>(st + 3 * TILE_BYTES + off);
-                pair_t x = mul2(ww1, v2.x), y = mul2(ww1, v2.y);
-                fma2(x, ww, v.x);
-                fma2(y, ww, v.y);
-                v.x = x;
-                v.y = y;
+                const float4 v2 = *reinterpret_cast<const float4*>(st + 3 * TILE_BYTES + off);
+                v = make_float4(fmaf(w, v.x, w1 * v2.x), fmaf(w, v.y, w1 * v2.y), fmaf(w, v.z, w1 * v2.z),
+                                fmaf(w, v.w, w1 * v2.w));
             }
 #pragma unroll
             for (int h4 = 0; h4 < NH / 4; ++h4) {
@@ -202,9 +172,10 @@ struct PagedF32 {
                 const float pw[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const pair_t pp = pack2(pw[x], pw[x]);
-                    fma2(o[4 * h4 + x][0], pp, v.x);
-                    fma2(o[4 * h4 + x][1], pp, v.y);
+                    o[4 * h4 + x][0] = fmaf(pw[x], v.x, o[4 * h4 + x][0]);
+                    o[4 * h4 + x][1] = fmaf(pw[x], v.y, o[4 * h4 + x][1]);
+                    o[4 * h4 + x][2] = fmaf(pw[x], v.z, o[4 * h4 + x][2]);
+                    o[4 * h4 + x][3] = fmaf(pw[x], v.w, o[4 * h4 + x][3]);
                 }
             }
         }
@@ -219,10 +190,7 @@ struct PagedF32 {
 #pragma unroll
             for (int h = 0; h < NH; ++h)
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float2 own = unpack2(o[h][x]), other = unpack2(__shfl_xor_sync(0xffffffffu, o[h][x], 16));
-                    o[h][x] = pack2(own.x + other.x, own.y + other.y);
-                }
+                for (int x = 0; x < 4; ++x) o[h][x] += __shfl_xor_sync(0xffffffffu, o[h][x], 16);
         __syncwarp();
         if ((lane & 7) == 0)
 #pragma unroll
@@ -236,10 +204,7 @@ struct PagedF32 {
     __device__ void values(F f) const {
         if (lane >= EL) return;
 #pragma unroll
-        for (int h = 0; h < NH; ++h) {
-            const float2 x = unpack2(o[h][0]), y = unpack2(o[h][1]);
-            f(h * EL + lane, make_float4(x.x, x.y, y.x, y.y));
-        }
+        for (int h = 0; h < NH; ++h) f(h * EL + lane, make_float4(o[h][0], o[h][1], o[h][2], o[h][3]));
     }
     __device__ static int2 heads(int k) { return make_int2(k / EL, k / EL); }
     __device__ static bool first_of(int k) { return k % EL == 0; }    // channel 0
