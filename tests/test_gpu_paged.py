@@ -49,6 +49,8 @@ DECODE = [
     ("bf16", 64, 2, 16, 16, [49, 200]),
     ("bf16", 128, 1, 8, 32, [4000]),                      # one unit over many CTAs
     ("bf16", 64, 8, 2, 16, [3, 5, 1, 16] * 40),           # far more units than CTAs
+    ("bf16", 128, 2, 4, 32, [0] * 40 + [5] + [0] * 60 + [700] + [0] * 30 + [16] * 50),   # idle rows between
+    ("bf16", 128, 4, 16, 64, [1500, 0, 900]),             # groups of 16 over several CTAs
     ("f32", 64, 2, 4, 16, RAGGED),
     ("f32", 64, 1, 7, 64, [300, 1, 0, 64, 65]),
     ("f32", 64, 2, 16, 32, [65, 31]),
