@@ -40,7 +40,7 @@
 
 namespace kvs {
 
-constexpr int PAGED_SMEM_MAX = 232448 - 3072;   // dynamic share of an SM's 227 KB (static beside it)
+constexpr int PAGED_SMEM_MAX = 224 * 1024;   // dynamic share of an SM's 227 KB (static beside it)
 
 // 4-D tiled bulk tensor load global -> shared with an L2 policy, completion counted on `bar`.
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
