@@ -15,8 +15,9 @@
 // table 32 entries at a time), keeping the online softmax of the unit it is in. A unit that
 // lies inside one warp's share is written out from registers. Otherwise the warps' states meet
 // in shared memory, and a unit that spans CTAs is joined by the last of them to arrive, from
-// one partial per CTA in L2 (two slots a CTA: the unit it ends and the unit it begins). Where
-// every unit is short and has a CTA of its own, it is not split across CTAs (launch_paged).
+// one partial per CTA in L2 (two slots a CTA: the unit it ends and the unit it begins). Short
+// shares are rounded to whole CTAs per unit, and where every unit is short and has a CTA of its
+// own, it is not split across CTAs at all (launch_paged).
 // K and V are read once and marked evict-first in L2 (64K-token decode 122 -> 120.5 us).
 //
 // Measured (one layer, replayed back to back; DRAM reads equal the algorithmic bytes):
@@ -173,6 +174,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     const bool early = a.aligned != 0 && list <= 32;         // the whole list, fetched beside the length
     unsigned share, more, t0;
     int my_n;
+    int unit_c0 = -1, unit_ctas = 0;             // whole CTAs per unit: this unit's first and how many
     if (a.aligned) {
         // one CTA per unit, its tiles dealt to the warps
         at.b = cta / a.Hkv;
@@ -192,6 +194,24 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         unsigned total = tiles_lane;
         for (int b = lane + 32; b < a.B; b += 32) total += row_tiles(row_len(b));
         const unsigned W = __reduce_add_sync(0xffffffffu, total) * a.Hkv;
+        const unsigned most = static_cast<unsigned>(a.ctas) * NW;
+        // Whole CTAs per unit where the shares are short and that costs a warp at most a tile more
+        // than an even share, or where few units make long joins: a CTA then joins one unit instead
+        // of up to two, one after the other. (5 requests of up to 8K, 4 heads: 19.8 -> 17.7 us; one
+        // of 64K, 4 heads: 34.9 -> 32.1; 2 of 5K, 8 heads: 17.0 -> 14.6. With longer shares and more
+        // units the uneven ends cost more: 30 of 3K, 4 heads: 26.4 -> 27.2.)
+        unsigned per_warp = 0;
+        const unsigned s0 = max(1u, (W + most - 1) / most);
+        if (a.B * a.Hkv <= (s0 <= 6 ? a.ctas : a.ctas / 8)) {
+            for (unsigned s = s0; s <= (s0 <= 6 ? s0 + 1 : s0) && per_warp == 0; ++s) {
+                unsigned n = 0;
+                for (int b = lane; b < a.B; b += 32)
+                    n += ((b == lane ? tiles_lane : row_tiles(row_len(b))) + NW * s - 1) / (NW * s);
+                if (__reduce_add_sync(0xffffffffu, n) * a.Hkv <= static_cast<unsigned>(a.ctas)) per_warp = s;
+            }
+        }
+        // the rows' lengths on the line: CTAs of NW * per_warp tiles, or tiles
+        const unsigned piece = per_warp > 0 ? NW * per_warp : 1;
         // no more CTAs than tiles: every CTA between a unit's first and last holds a part of it
         const unsigned nc = max(1u, min(static_cast<unsigned>(a.ctas), (W + NW - 1) / NW));
         const unsigned workers = nc * NW;
@@ -200,29 +220,44 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         const unsigned id = cta * NW + warp;
         t0 = share * id + min(id, more);
         my_n = id < workers ? share + (id < more ? 1 : 0) : 0;
+        const unsigned target = per_warp > 0 ? cta : t0;
         unsigned base = 0;
-        for (int r0 = 0; my_n > 0 && r0 < a.B; r0 += 32) {
+        bool found = false;
+        for (int r0 = 0; !found && r0 < a.B && (per_warp > 0 || my_n > 0); r0 += 32) {
             const int n = r0 == 0 ? n_lane : r0 + lane < a.B ? row_len(r0 + lane) : 0;
             const int own = r0 == 0 ? tiles_lane : row_tiles(n);
-            unsigned incl = static_cast<unsigned>(own) * a.Hkv;
+            const unsigned pieces = per_warp > 0 ? (own + piece - 1) / piece : own;
+            unsigned incl = pieces * a.Hkv;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const unsigned x = __shfl_up_sync(0xffffffffu, incl, off);
                 if (lane >= off) incl += x;
             }
-            const unsigned ahead = __ballot_sync(0xffffffffu, base + incl > t0);
+            const unsigned ahead = __ballot_sync(0xffffffffu, base + incl > target);
             if (ahead != 0u) {
                 const int who = __ffs(ahead) - 1;
                 at.b = r0 + who;
                 at.n = __shfl_sync(0xffffffffu, n, who);
                 at.tiles = __shfl_sync(0xffffffffu, own, who);
-                const unsigned in_row = t0 - (base + __shfl_sync(0xffffffffu, incl, who) - static_cast<unsigned>(at.tiles) * a.Hkv);
-                at.j = in_row / at.tiles;
-                at.t = in_row - at.j * at.tiles;
-                break;
+                const unsigned m = __shfl_sync(0xffffffffu, pieces, who);
+                const unsigned in_row = target - (base + __shfl_sync(0xffffffffu, incl, who) - m * a.Hkv);
+                at.j = in_row / m;
+                at.t = in_row - at.j * m;
+                if (per_warp > 0) {              // CTA at.t of the unit's m: its warps' part of the unit
+                    unit_c0 = cta - at.t;
+                    unit_ctas = m;
+                    const unsigned all = m * NW, me = at.t * NW + warp;
+                    share = at.tiles / all;
+                    more = at.tiles - share * all;
+                    t0 = share * me + min(me, more);
+                    my_n = share + (me < more ? 1 : 0);
+                    at.t = t0;
+                }
+                found = true;
             }
             base += __shfl_sync(0xffffffffu, incl, 31);
         }
+        if (!found) my_n = 0;
     }
     // to the next unit that has tiles (only called while the share holds more)
     auto next_unit = [&](Cursor& c) {
@@ -395,8 +430,8 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         };
         int* part = s_part[flags_l & 1];
         part[0] = unit_l;
-        part[1] = owner(mine.begin);
-        part[2] = owner(mine.begin + mine.tiles - 1) - part[1] + 1;
+        part[1] = unit_c0 >= 0 ? unit_c0 : owner(mine.begin);
+        part[2] = unit_c0 >= 0 ? unit_ctas : owner(mine.begin + mine.tiles - 1) - part[1] + 1;
     }
     constexpr int per = paged_partial(NH, D), VALS = P::VALS;
     static_assert(VALS * 4 == NH * D, "a state's values");

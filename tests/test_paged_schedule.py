@@ -51,6 +51,46 @@ def test_join_counts_match_the_shares(seed):
     assert all(s < 2 * ctas for s in slots)
 
 
+@pytest.mark.parametrize("seed", range(60))
+def test_whole_ctas_per_unit_cover_every_tile_once(seed):
+    r = random.Random(1000 + seed)
+    nw, ctas, heads = r.choice([2, 4, 8, 12]), r.choice([17, 148]), r.choice([1, 2, 5, 8])
+    top = r.choice([3, 30, 900])
+    rows = [r.choice([0, 1, r.randrange(0, top)]) for _ in range(r.randrange(1, ctas // heads + 1))]
+    W = sum(rows) * heads
+    most = ctas * nw
+    s0 = max(1, -(-W // most))
+    if len(rows) * heads > (ctas if s0 <= 6 else ctas // 8):
+        return
+    for s in range(s0, s0 + (2 if s0 <= 6 else 1)):
+        pieces = [-(-t // (nw * s)) for t in rows]
+        if sum(pieces) * heads <= ctas:
+            break
+    else:
+        return
+    seen = [[set() for _ in range(heads)] for _ in rows]
+    for cta in range(ctas):
+        base = 0
+        for b, m in enumerate(pieces):
+            if base + m * heads > cta:
+                j, seg = divmod(cta - base, m)
+                share, more = divmod(rows[b], m * nw)
+                mine = 0
+                for w in range(nw):
+                    me = seg * nw + w
+                    t0 = share * me + min(me, more)
+                    n = share + (1 if me < more else 0)
+                    tiles = set(range(t0, t0 + n))
+                    assert not tiles & seen[b][j] and n <= s + 1
+                    seen[b][j] |= tiles
+                    mine += n
+                assert mine > 0                                  # every CTA of a unit takes part in its join
+                break
+            base += m * heads
+    for b, t in enumerate(rows):
+        assert all(x == set(range(t)) for x in seen[b])
+
+
 def test_windows_of_page_entries_cover_a_tile():
     # 32 entries from a tile's first block: the tile's later pieces stay inside the window
     for page, tile in ((16, 16), (16, 32), (32, 32), (64, 32), (128, 16), (256, 32)):
