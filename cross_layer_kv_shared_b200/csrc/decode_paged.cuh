@@ -200,33 +200,39 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         // of up to two, one after the other. (5 requests of up to 8K, 4 heads: 19.8 -> 17.7 us; one
         // of 64K, 4 heads: 34.9 -> 32.1; 2 of 5K, 8 heads: 17.0 -> 14.6. With longer shares and more
         // units the uneven ends cost more: 30 of 3K, 4 heads: 26.4 -> 27.2.)
+        auto pieces_of = [&](unsigned tiles, unsigned s) {   // CTAs of NW * s tiles; division by a constant at s = 1
+            return s == 1 ? (tiles + NW - 1) / NW : (tiles + NW * s - 1) / (NW * s);
+        };
         unsigned per_warp = 0;
-        const unsigned s0 = max(1u, (W + most - 1) / most);
+        const unsigned s0 = W <= most ? 1u : (W + most - 1) / most;
         if (a.B * a.Hkv <= (s0 <= 6 ? a.ctas : a.ctas / 8)) {
             for (unsigned s = s0; s <= (s0 <= 6 ? s0 + 1 : s0) && per_warp == 0; ++s) {
                 unsigned n = 0;
                 for (int b = lane; b < a.B; b += 32)
-                    n += ((b == lane ? tiles_lane : row_tiles(row_len(b))) + NW * s - 1) / (NW * s);
+                    n += pieces_of(b == lane ? tiles_lane : row_tiles(row_len(b)), s);
                 if (__reduce_add_sync(0xffffffffu, n) * a.Hkv <= static_cast<unsigned>(a.ctas)) per_warp = s;
             }
         }
-        // the rows' lengths on the line: CTAs of NW * per_warp tiles, or tiles
-        const unsigned piece = per_warp > 0 ? NW * per_warp : 1;
-        // no more CTAs than tiles: every CTA between a unit's first and last holds a part of it
-        const unsigned nc = max(1u, min(static_cast<unsigned>(a.ctas), (W + NW - 1) / NW));
-        const unsigned workers = nc * NW;
-        share = W / workers;
-        more = W - share * workers;              // the first `more` warps take one tile more
-        const unsigned id = cta * NW + warp;
-        t0 = share * id + min(id, more);
-        my_n = id < workers ? share + (id < more ? 1 : 0) : 0;
+        share = more = t0 = 0;
+        my_n = 0;
+        if (per_warp == 0) {
+            // no more CTAs than tiles: every CTA between a unit's first and last holds a part of it
+            const unsigned nc = max(1u, min(static_cast<unsigned>(a.ctas), (W + NW - 1) / NW));
+            const unsigned workers = nc * NW;
+            share = W / workers;
+            more = W - share * workers;          // the first `more` warps take one tile more
+            const unsigned id = cta * NW + warp;
+            t0 = share * id + min(id, more);
+            my_n = id < workers ? share + (id < more ? 1 : 0) : 0;
+        }
+        // where this CTA or this warp's first tile lies on the line of the rows
         const unsigned target = per_warp > 0 ? cta : t0;
         unsigned base = 0;
         bool found = false;
         for (int r0 = 0; !found && r0 < a.B && (per_warp > 0 || my_n > 0); r0 += 32) {
             const int n = r0 == 0 ? n_lane : r0 + lane < a.B ? row_len(r0 + lane) : 0;
             const int own = r0 == 0 ? tiles_lane : row_tiles(n);
-            const unsigned pieces = per_warp > 0 ? (own + piece - 1) / piece : own;
+            const unsigned pieces = per_warp > 0 ? pieces_of(own, per_warp) : own;
             unsigned incl = pieces * a.Hkv;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
