@@ -357,6 +357,8 @@ SELECT = [
     ("bf16", 64, 1, 2, 16, [40000], 64, 1, 1, False),          # 2500 blocks: 512 threads
     ("bf16", 64, 1, 8, 16, [70000], 7, 1, 1, False),           # 4375 blocks: 1024 threads
     ("bf16", 64, 2, 2, 16, [100, 100], 7, 1, 1, False),        # every block kept: no scores needed
+    ("bf16", 128, 1, 4, 128, [200, 0, 17], 3, 1, 1, True),     # lists longer than the block table's rows
+    ("f32", 64, 2, 1, 16, [70, 33], 12, 2, 3, False),
 ]
 
 
@@ -716,3 +718,22 @@ def test_refusals_launch_nothing(K):
         assert K.kvshare_launch_count(h) == n0 and K.kvshare_sync_status(h) == K.KVS_OK
     finally:
         K.kvshare_destroy(h)
+
+
+# -------------------------------------------------------------------------------- example
+def test_the_readme_example_of_a_paged_cache_runs():
+    import os
+    import re
+    torch = torch_mod()
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "README.md")) as f:
+        blocks = re.findall(r"```python\n(.*?)```", f.read(), re.S)
+    paged_block = [b for b in blocks if "kvshare_plan_pages" in b]
+    assert len(paged_block) == 1
+    names = {}
+    exec(compile(paged_block[0], "README.md", "exec"), names)      # noqa: S102  (the repository's own text)
+    # one token each: every head's output is its kv head's value, the softmax of one score being 1
+    qkv, out = names["qkv"], names["out"]
+    assert torch.isfinite(out).all() and names["lens"].tolist() == [1] * 32
+    assert names["v"][10, names["table"][:, 0].long(), :, 0].repeat_interleave(8, dim=1).float().equal(out[21])
+    assert qkv.shape[0] == 32
