@@ -731,9 +731,12 @@ def test_the_readme_example_of_a_paged_cache_runs():
     paged_block = [b for b in blocks if "kvshare_plan_pages" in b]
     assert len(paged_block) == 1
     names = {}
+    torch.manual_seed(0)
     exec(compile(paged_block[0], "README.md", "exec"), names)      # noqa: S102  (the repository's own text)
-    # one token each: every head's output is its kv head's value, the softmax of one score being 1
-    qkv, out = names["qkv"], names["out"]
-    assert torch.isfinite(out).all() and names["lens"].tolist() == [1] * 32
-    assert names["v"][10, names["table"][:, 0].long(), :, 0].repeat_interleave(8, dim=1).float().equal(out[21])
-    assert qkv.shape[0] == 32
+    # one token each: every head's output is its kv head's value v. The one weight p divides itself
+    # out: (p v) (1 / p) with p's three parts and their sum off by at most 6 half steps together
+    # (remainder 1, tensor-core sums 4, joining sum 1), reciprocal and product 1 each: 2^-21
+    out, v = names["out"], names["v"]
+    assert names["lens"].tolist() == [1] * 32
+    want = v[10, names["table"][:, 0].long(), :, 0].repeat_interleave(8, dim=1).float()
+    assert ((out[21] - want).abs() <= want.abs() * 2.0 ** -21).all()
