@@ -8,7 +8,8 @@
 //   the ring's last in (sequence, block) order: the two stretches never overlap, so no block
 //   of the launch waits for another
 //   token i of the step (sequences end to end): position n_b + (i - start_b), slot =
-//   page(position / page) * page + position % page; entries behind the last token get -1
+//   page(position / page) * page + position % page; entries behind the last token get -1, and
+//   so do tokens whose page lies outside the pool (reported)
 // A few loads and prefix sums: bound by latency for a decode step and by the writes of the
 // token arrays for prompts. Every block repeats the prefix sums over the sequences (a few
 // microseconds at most) and fills its share of the token arrays; the last block to have read
@@ -185,6 +186,11 @@ __global__ void __launch_bounds__(NT) plan_pages_kernel(const PagePlanArgs a) {
         while (x >= a.num_pages) x -= a.num_pages;
         return static_cast<int>(x);
     };
+    auto exists = [&](int page) {         // reports a page outside the pool
+        const bool ok = page >= 0 && page < a.num_pages;
+        if (!ok) atomicOr(a.err, ERR_RANGE);
+        return ok;
+    };
     auto last_at_or_before = [&](const int* from, int x) {   // the last sequence with from[b] <= x
         int lo = 0, hi = a.B - 1;
         while (lo < hi) {
@@ -206,7 +212,8 @@ __global__ void __launch_bounds__(NT) plan_pages_kernel(const PagePlanArgs a) {
             int* entry = a.table + static_cast<size_t>(lo) * a.max_blocks + blk;
             const int page = k < 0 ? *entry : a.ring[ring_at(s_new[lo] + k)];
             if (k >= 0 && (pos & (ps - 1)) == 0) *entry = page;
-            slot = page * ps + (pos & (ps - 1));
+            // a page the pool does not have: no slot. Its product with the page size could wrap to another page's row
+            if (exists(page)) slot = page * ps + (pos & (ps - 1));
         }
         a.slot_map[i] = slot;
         a.position[i] = pos;
@@ -214,7 +221,9 @@ __global__ void __launch_bounds__(NT) plan_pages_kernel(const PagePlanArgs a) {
     // ---- pages that return, dealt evenly over the grid
     for (int r = blockIdx.x * NT + threadIdx.x; r < s_total[2]; r += gridDim.x * NT) {
         const int b = last_at_or_before(s_backx, r);
-        a.ring[ring_at(count + r)] = a.table[static_cast<size_t>(b) * a.max_blocks + (r - s_backx[b])];
+        const int page = a.table[static_cast<size_t>(b) * a.max_blocks + (r - s_backx[b])];
+        exists(page);                     // reported; it keeps its place, so the count stands
+        a.ring[ring_at(count + r)] = page;
     }
 }
 

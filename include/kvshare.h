@@ -318,8 +318,10 @@ kvshare_status kvshare_append_lowrank(kvshare_t ctx, const kvshare_cache* cache,
  * for fit max_tokens; otherwise it takes nothing (length unchanged) and the next
  * kvshare_sync_status returns KVS_ENOMEM. A sequence that would pass max_blocks *
  * page_size takes nothing, and more returning pages than the pool has room for are
- * dropped; both report KVS_EINVAL. lengths_out may be lengths and ring_state_out
- * ring_state; no other two arrays may overlap. A page belongs to one sequence at a time.
+ * dropped; both report KVS_EINVAL. So does a page outside [0, num_pages) that the table or
+ * the ring names: its tokens get slot -1, and it keeps its place in table and ring.
+ * lengths_out may be lengths and ring_state_out ring_state; no other two arrays may
+ * overlap. A page belongs to one sequence at a time.
  * batch <= 4096 (KVS_EUNSUPPORTED above); batch * max_blocks and num_pages * page_size below
  * 2^31, max_blocks * page_size and max_tokens at most 2^30. */
 kvshare_status kvshare_plan_pages(kvshare_t ctx, const int* lengths, const int* new_tokens, int* block_table,

@@ -9,8 +9,12 @@ import math
 import numpy as np
 
 
-def plan(lengths, new_tokens, table, ring, head, count, page, max_tokens):
-    """Returns a dict of the outputs and the set of faults ('range', 'pool') the step reports."""
+def plan(lengths, new_tokens, table, ring, head, count, page, max_tokens, num_pages=None):
+    """Returns a dict of the outputs and the set of faults ('range', 'pool') the step reports.
+
+    A page outside [0, num_pages) is reported: its tokens get no slot, and it keeps its place where it
+    returns to the ring. None: no page is looked at.
+    """
     table, ring = [list(r) for r in table], list(ring)
     B, blocks, N = len(lengths), len(table[0]), len(ring)
     cap = blocks * page
@@ -20,6 +24,12 @@ def plan(lengths, new_tokens, table, ring, head, count, page, max_tokens):
     out_len, start, slots, pos = [], [0], [], []
     room = N - count
     given = 0
+
+    def exists(p):
+        if num_pages is None or 0 <= p < num_pages:
+            return True
+        faults.add("range")
+        return False
     for b in range(B):
         n, m = int(lengths[b]), int(new_tokens[b])
         if n < 0 or n > cap:
@@ -33,6 +43,7 @@ def plan(lengths, new_tokens, table, ring, head, count, page, max_tokens):
             else:
                 for i in range(held):
                     # entries behind the ring's last, in order
+                    exists(old_table[b][i])
                     ring[(head + count + given - held + i) % N] = old_table[b][i]
                 returned += held
             out_len.append(0)
@@ -53,7 +64,8 @@ def plan(lengths, new_tokens, table, ring, head, count, page, max_tokens):
             table[b][held + i] = ring[(head + taken + i) % N]
         taken += need
         for t in range(n, n + want):
-            slots.append(table[b][t // page] * page + t % page)
+            p = table[b][t // page]
+            slots.append(p * page + t % page if exists(p) else -1)
             pos.append(t)
         out_len.append(n + want)
         start.append(len(slots))
