@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(NT) plan_pages_kernel(const PagePlanArgs a) {
             const int m = a.new_tokens[b];
             if (len < 0 || len > cap) {
                 err |= ERR_RANGE;
-                len = len < 0 ? 0 : static_cast<int>(cap);
+                len = m < 0 || len < 0 ? 0 : static_cast<int>(cap);   // which pages such a sequence holds is unknown: none returns
             }
             n[e] = len;
             held[e] = (len + ps - 1) >> a.page_shift;

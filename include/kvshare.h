@@ -300,7 +300,8 @@ kvshare_status kvshare_append_lowrank(kvshare_t ctx, const kvshare_cache* cache,
 
 /* Pages and slots of one step of a paged cache, planned on the GPU from the sequences'
  * lengths, so that a captured step needs no host. All arrays are int32 DEVICE arrays.
- *   lengths     [batch] cached tokens n_b
+ *   lengths     [batch] cached tokens n_b; one outside [0, max_blocks * page_size] is clamped and
+ *               reported as KVS_EINVAL, and no page returns if its sequence leaves
  *   new_tokens  [batch] tokens m_b sequence b takes now; m_b < 0: the sequence leaves
  *   block_table [batch][max_blocks], in place: entries of new blocks are written
  *   ring        [num_pages] free pages, in place: `count` of them from entry `head` on,

@@ -34,7 +34,7 @@ def plan(lengths, new_tokens, table, ring, head, count, page, max_tokens, num_pa
         n, m = int(lengths[b]), int(new_tokens[b])
         if n < 0 or n > cap:
             faults.add("range")
-            n = min(max(n, 0), cap)
+            n = min(max(n, 0), cap) if m >= 0 else 0        # nobody knows the pages of one that leaves
         held = -(-n // page)
         if m < 0:
             given += held

@@ -84,3 +84,15 @@ def test_no_other_row_is_written_for_a_page_outside_the_pool(K, ctx):
     for x, was in zip((k, v), before):
         was[0, 1, :, 7] = 7.0
         assert torch.equal(x.view(torch.int16), was.view(torch.int16))
+
+
+@pytest.mark.parametrize("length", [33, 2 ** 31 - 1, -1, -2 ** 31])
+def test_a_leaving_sequence_of_unknown_length_returns_no_page(K, ctx, length):
+    """Clamped to its row of the table it would put whatever the row holds into the ring, pages of others too."""
+    table = [[3, 1], [1, -1]]                          # the second entry of row 0 is stale: page 1 is row 1's
+    ring = [9, 8, 0, 0, 0, 0, 0, 0, 0, 0]
+    want, faults = paged.plan([length, 4], [-1, 1], table, ring, 0, 2, 16, 8, num_pages=10)
+    got, st = plan_on_gpu(K, ctx, [length, 4], [-1, 1], table, ring, 0, 2, 16, 8)
+    assert st == K.KVS_EINVAL and faults == {"range"}
+    assert got["ring_state"] == [0, 2] and got["ring"] == ring and got["lengths"] == [0, 5]
+    agree(got, want)

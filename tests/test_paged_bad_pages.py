@@ -23,3 +23,9 @@ def test_the_wrapped_slot_of_such_a_page_lies_in_the_pool():
     # what 32-bit arithmetic makes of page 0x10000001 at 16 tokens a page: row 1 of page 1
     wrapped = (0x10000001 * 16 + 1) % 2 ** 32
     assert wrapped == 17
+
+
+@pytest.mark.parametrize("length", [9, 2 ** 31 - 1, -1])
+def test_a_leaving_sequence_of_unknown_length_returns_no_page(length):
+    out, faults = paged.plan([length, 3], [-1, 0], [[3, 1], [1, -1]], [0, 2, 0, 0], 0, 2, 4, 4, num_pages=4)
+    assert faults == {"range"} and out["ring"] == [0, 2, 0, 0] and out["ring_state"] == [0, 2] and out["lengths"] == [0, 3]
