@@ -842,11 +842,14 @@ kvshare_status kvshare_sync_status(kvshare_t ctx, void* stream) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return KVS_ECUDA;
     unsigned word = 0;
     if (cudaMemcpy(&word, ctx->err, sizeof(unsigned), cudaMemcpyDeviceToHost) != cudaSuccess) return KVS_ECUDA;
-    if (word != 0) {
-        if (cudaMemset(ctx->err, 0, sizeof(unsigned)) != cudaSuccess) return KVS_ECUDA;
-        if (word & ERR_TIMEOUT) return KVS_ETIMEOUT;
-        if (word & ERR_RANGE) return KVS_EINVAL;
-        if (word & ERR_POOL) return KVS_ENOMEM;
+    // one kind of fault a call: the others stay recorded for the next ones
+    const struct { unsigned bit; kvshare_status status; } kinds[] = {
+        {ERR_TIMEOUT, KVS_ETIMEOUT}, {ERR_RANGE, KVS_EINVAL}, {ERR_POOL, KVS_ENOMEM}};
+    for (const auto& k : kinds) {
+        if (!(word & k.bit)) continue;
+        word &= ~k.bit;
+        if (cudaMemcpy(ctx->err, &word, sizeof(unsigned), cudaMemcpyHostToDevice) != cudaSuccess) return KVS_ECUDA;
+        return k.status;
     }
     return KVS_OK;
 }

@@ -377,11 +377,12 @@ kvshare_status kvshare_decode_paged(kvshare_t ctx, const kvshare_pages* pages, c
 kvshare_status kvshare_select_pages(kvshare_t ctx, const kvshare_pages* pages, const void* q, int* selected,
                                     int top, int first, int last, int l0, int l1, void* stream);
 
-/* Synchronise `stream`, then read and clear the device status word.
+/* Synchronise `stream`, then read the device status word and clear what is returned.
  * Returns KVS_OK, KVS_ETIMEOUT (a bounded device wait ran out), KVS_EINVAL (a
  * per-sequence length outside [0, context] was clamped, or an index outside a paged
  * cache was skipped), KVS_ENOMEM (kvshare_plan_pages did not admit a sequence) or
- * KVS_ECUDA. */
+ * KVS_ECUDA. Where more than one of them was recorded, a call returns the first in this
+ * order and the next call the next one, until KVS_OK. */
 kvshare_status kvshare_sync_status(kvshare_t ctx, void* stream);
 
 /* Split-KV override for decode: 0 = automatic (default), n > 0 = n splits per

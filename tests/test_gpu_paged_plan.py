@@ -96,3 +96,29 @@ def test_a_leaving_sequence_of_unknown_length_returns_no_page(K, ctx, length):
     assert st == K.KVS_EINVAL and faults == {"range"}
     assert got["ring_state"] == [0, 2] and got["ring"] == ring and got["lengths"] == [0, 5]
     agree(got, want)
+
+
+def test_two_kinds_of_fault_are_both_reported(K, ctx):
+    """One sequence past its row of the table, another without pages: neither report is lost."""
+    table, ring = [[0, -1], [1, -1]], [2, 3, 0, 0]
+    want, faults = paged.plan([16, 16], [17, 1], table, ring, 0, 0, 16, 32, num_pages=4)
+    got, st = plan_on_gpu(K, ctx, [16, 16], [17, 1], table, ring, 0, 0, 16, 32)
+    assert faults == {"range", "pool"}
+    agree(got, want)
+    assert st == K.KVS_EINVAL
+    assert K.kvshare_sync_status(ctx) == K.KVS_ENOMEM
+    assert K.kvshare_sync_status(ctx) == K.KVS_OK
+    # a time-out on top of both: all three, one a call
+    K.kvshare_debug_stall_next(ctx, True)
+    torch = torch_mod()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    t = lambda x: torch.tensor(x, **i32)  # noqa: E731
+    state, start, slots = t([0, 0]), torch.zeros(3, **i32), torch.zeros(32, **i32)
+    K.kvshare_plan_pages(ctx, t([16, 16]), t([17, 1]), t(table), t(ring), state, torch.zeros(2, **i32),
+                         torch.zeros(2, **i32), start, slots, torch.zeros(32, **i32), 16)
+    kv = torch.zeros(1, 4, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(1, 2, 2, 64, dtype=torch.bfloat16, device="cuda")
+    K.kvshare_decode_paged(ctx, K.Pages(k=kv, v=kv, block_table=t([[0, 1], [2, 3]]), lengths=t([3, 0])), q,
+                           torch.zeros(q.shape, device="cuda"))
+    seen = [K.kvshare_sync_status(ctx) for _ in range(4)]
+    assert seen == [K.KVS_ETIMEOUT, K.KVS_EINVAL, K.KVS_ENOMEM, K.KVS_OK]
