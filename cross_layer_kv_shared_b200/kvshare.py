@@ -139,6 +139,11 @@ def kvshare_create(num_layers: int, num_q_heads: int, num_kv_heads: int, head_di
     return st, h
 
 
+def _config(h):
+    """The sizes of a live context, by its handle (the c_void_p or its value), or None."""
+    return _configs.get(getattr(h, "value", h))
+
+
 def kvshare_destroy(h) -> int:
     _configs.pop(getattr(h, "value", h), None)
     return _lib.kvshare_destroy(h)
@@ -345,7 +350,7 @@ def kvshare_plan_pages(h, lengths, new_tokens, block_table, ring, ring_state, le
 
 def kvshare_append_paged(h, pages: Pages, slot: int, k_new, v_new, slot_map, stream=None, check: bool = True) -> int:
     """k_new, v_new: [tokens][Hkv][d], each token's heads dense; the tokens may be rows of a wider tensor."""
-    st, cfg, model = KVS_EINVAL, _configs.get(h.value), pages._model
+    st, cfg, model = KVS_EINVAL, _config(h), pages._model
     if cfg is not None and cfg[1] == model:
         n, H, d = slot_map.numel(), model[0], model[1]
         dt, shape = pages._dtype, (n, H, d)
@@ -364,7 +369,7 @@ def kvshare_append_paged(h, pages: Pages, slot: int, k_new, v_new, slot_map, str
 
 def kvshare_decode_paged(h, pages: Pages, q, out, lse=None, l0: int = 0, l1: int = None, selected=None, stream=None,
                          check: bool = True) -> int:
-    st, cfg = KVS_EINVAL, _configs.get(h.value)
+    st, cfg = KVS_EINVAL, _config(h)
     got = _layer_range(pages, cfg, q, l1) if cfg is not None and cfg[1] == pages._model else None
     if got is not None:
         (shape, l1), float32, top, sp = got, _torch.float32, 0, None
@@ -384,7 +389,7 @@ def kvshare_decode_paged(h, pages: Pages, q, out, lse=None, l0: int = 0, l1: int
 
 def kvshare_select_pages(h, pages: Pages, q, selected, first: int = 1, last: int = 1, l0: int = 0, l1: int = None,
                          stream=None, check: bool = True) -> int:
-    st, cfg = KVS_EINVAL, _configs.get(h.value)
+    st, cfg = KVS_EINVAL, _config(h)
     got = _layer_range(pages, cfg, q, l1) if cfg is not None and cfg[1] == pages._model else None
     if got is not None:
         (shape, l1), top = got, selected.shape[-1]
