@@ -180,7 +180,7 @@ kvshare_status kvshare_append_paged(kvshare_t ctx, const kvshare_pages* pages, i
     a.num_pages = pages->num_pages;
     a.f32 = cf.dtype == KVS_F32;
     a.err = ctx->err;
-    if (launch_append_paged(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return KVS_ECUDA;
+    if (launch_append_paged(a, ctx->sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) return KVS_ECUDA;
     ++ctx->launches;
     return KVS_OK;
 }

@@ -204,20 +204,20 @@ __global__ void __launch_bounds__(NT) append_paged_kernel(const PagedAppendArgs 
 }
 
 template <bool F32, int RB>
-cudaError_t launch(const PagedAppendArgs& a, cudaStream_t st) {
+cudaError_t launch(const PagedAppendArgs& a, int sms, cudaStream_t st) {
     Grid gr;
     // copy blocks: every thread has up to UNROLL pieces in flight; fewer when that would leave
-    // multiprocessors idle
+    // fewer than two blocks a multiprocessor
     const int per = 2 * a.Hkv * (RB / 16);
     const int side = per >= NT ? 1 : NT / per;
     int tokens = side * UNROLL;
-    while (tokens > side && (a.tokens + tokens - 1) / tokens < 296) tokens = (tokens / side + 1) / 2 * side;
+    while (tokens > side && (a.tokens + tokens - 1) / tokens < 2 * sms) tokens = (tokens / side + 1) / 2 * side;
     gr.copy_tokens = tokens;
     int blocks = (a.tokens + tokens - 1) / tokens;
     gr.bound_tokens = 1;
     gr.bound_blocks = 0;
     if (a.codes != nullptr) {
-        const int bt = (a.tokens + 591) / 592;
+        const int bt = (a.tokens + 4 * sms - 1) / (4 * sms);    // four blocks a multiprocessor, at most 32 tokens each
         gr.bound_tokens = bt > 32 ? 32 : bt;
         gr.bound_blocks = (a.tokens + gr.bound_tokens - 1) / gr.bound_tokens;
         blocks += gr.bound_blocks;
@@ -227,9 +227,9 @@ cudaError_t launch(const PagedAppendArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_append_paged(const PagedAppendArgs& a, cudaStream_t st) {
-    if (a.f32) return a.d == 64 ? launch<true, 256>(a, st) : launch<true, 512>(a, st);
-    return a.d == 64 ? launch<false, 128>(a, st) : launch<false, 256>(a, st);
+cudaError_t launch_append_paged(const PagedAppendArgs& a, int sms, cudaStream_t st) {
+    if (a.f32) return a.d == 64 ? launch<true, 256>(a, sms, st) : launch<true, 512>(a, sms, st);
+    return a.d == 64 ? launch<false, 128>(a, sms, st) : launch<false, 256>(a, sms, st);
 }
 
 }  // namespace kvs

@@ -76,7 +76,7 @@ struct PagedAppendArgs {
     bool f32;
     unsigned* err;
 };
-cudaError_t launch_append_paged(const PagedAppendArgs& a, cudaStream_t st);
+cudaError_t launch_append_paged(const PagedAppendArgs& a, int sms, cudaStream_t st);
 
 // Pages and slots of a step.
 struct PagePlanArgs {
