@@ -1,9 +1,11 @@
 // Block selection of a paged decode: a cheap score of every page against the query, and the
-// best `top` blocks of each (sequence, kv head).
+// best `top` blocks of each (sequence, kv head). Ranking pages by per-channel extremes of their
+// keys is a published idea (query-aware page selection, Tang et al., 2024).
 //
 //   query codes of head h:  s_q = fl(1/127) max_c |q_c|, c_q = rint(q / s_q)
-//   page p:                 dot = sum_c (c_q > 0 ? c_q hi_c : c_q lo_c), an upper bound of
-//                           q . k over the page's keys, in whole numbers
+//   page p:                 dot = sum_c (c_q > 0 ? c_q hi_c : c_q lo_c): times both scales an
+//                           upper bound of q~ . k over the page's keys, q~ = s_q c_q the rounded
+//                           query; q . k may lie above it by at most s_q / 2 sum |k|
 //   score_h = (dot s_q) s_p;  MIX: w score_h1 + (1 - w) score_h2;  score = max over the group
 // The dot product is the whole-number product of [max(c_q, 0) | min(c_q, 0)] with [hi | lo]
 // (below 2^22, exact in fp32 whatever the order), and every fp32 step after it is one IEEE

@@ -136,7 +136,8 @@ typedef struct {
  * block_table and lengths are read on the device: a length outside [0, max_blocks *
  * page_size] is clamped, a page outside [0, num_pages) reads as zeros and is never written,
  * and either makes the next kvshare_sync_status return KVS_EINVAL. Block-table entries past
- * a sequence's last block are not read. Tokens past its length may hold anything (NaN).
+ * a sequence's last block are not used (they may be loaded: a row's max_blocks entries are
+ * memory, of any content). Tokens past its length may hold anything (NaN).
  * num_pages * page_size and slots * num_pages * Hkv must stay below 2^31 and max_blocks *
  * page_size at most 2^30; byte offsets are 64-bit. batch <= max_batch and (max_blocks - 1) * page_size < max_context of the context. */
 typedef struct {
@@ -305,7 +306,9 @@ kvshare_status kvshare_append_lowrank(kvshare_t ctx, const kvshare_cache* cache,
  *   new_tokens  [batch] tokens m_b sequence b takes now; m_b < 0: the sequence leaves
  *   block_table [batch][max_blocks], in place: entries of new blocks are written
  *   ring        [num_pages] free pages, in place: `count` of them from entry `head` on,
- *               modulo num_pages; ring_state = {head, count}
+ *               modulo num_pages; ring_state = {head, count}, 0 <= head < num_pages, 0 <= count
+ *               <= num_pages (any other state is an empty ring without room and is reported as
+ *               KVS_EINVAL)
  *   lengths_out [batch]: n_b + m_b, or 0 for a sequence that leaves
  *   ring_state_out [2]; token_start [batch + 1]: first new token of each sequence, then
  *               their total
@@ -353,8 +356,9 @@ kvshare_status kvshare_append_paged(kvshare_t ctx, const kvshare_pages* pages, i
  *   q, out, lse: as in kvshare_decode (lse may be NULL)
  *   selected:    [L][batch][Hkv][top] int32 DEVICE block indices to attend to, as written by
  *                kvshare_select_pages (distinct; the first min(top, blocks of b) entries of a
- *                row are read, in any order; one outside the sequence's blocks is skipped
- *                and reported as KVS_EINVAL), or NULL: every block
+ *                row are used, in any order; one outside the sequence's blocks is skipped
+ *                and reported as KVS_EINVAL; later entries may be anything), or NULL: every
+ *                block
  * Sequences of any mix of lengths share the GPU evenly: the split is computed on the
  * device from the lengths, and the joins run in a fixed order, so the same inputs give the
  * same bits. Attention weights enter the P.V product with 24 bits: results differ from
@@ -367,13 +371,15 @@ kvshare_status kvshare_decode_paged(kvshare_t ctx, const kvshare_pages* pages, c
  * head) the `first` first blocks, the `last` last ones and those with the highest score, in
  * ascending order, min(top, blocks) of them and then -1; ties go to the lowest block.
  *   selected: [L][batch][Hkv][top] int32 DEVICE
- * The score of a page bounds q . k over its keys from above, in int8: with q's codes c =
- * rint(q / s_q), s_q = max |q| * (1/127) per head, dot = sum_c (c > 0 ? c hi : c lo) over the
- * page's bound codes and score = (dot * s_q) * bound_scale, each step one fp32 operation;
- * for a MIX layer w * score_1 + (1 - w) * score_2; the largest over the group's heads.
+ * The score of a page is an estimate in int8 of the largest q . k over its keys: with q's
+ * codes c = rint(q / s_q), s_q = max |q| * (1/127) per head, dot = sum_c (c > 0 ? c hi : c lo)
+ * over the page's bound codes and score = (dot * s_q) * bound_scale, each step one fp32
+ * operation; for a MIX layer w * score_1 + (1 - w) * score_2; the largest over the group's
+ * heads. Up to those roundings it bounds q~ . k from above for the rounded query q~ = s_q c;
+ * q . k itself may lie above it by at most s_q / 2 * sum |k|.
  * Selections are reproducible bit for bit. 0 <= first, 1 <= last, first + last <= top,
- * max_blocks <= 16384 (KVS_EUNSUPPORTED above). Layers that share a source may share a
- * selection. */
+ * max_blocks <= 16384 (KVS_EUNSUPPORTED above). A decode of layer l reads row l of
+ * `selected`: to let a layer use another's choice, copy that row. */
 kvshare_status kvshare_select_pages(kvshare_t ctx, const kvshare_pages* pages, const void* q, int* selected,
                                     int top, int first, int last, int l0, int l1, void* stream);
 
