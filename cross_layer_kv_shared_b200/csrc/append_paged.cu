@@ -14,8 +14,9 @@
 // neighbouring threads write neighbouring bytes. Bound blocks: a warp per (page, head) reads
 // the new rows from the input and the earlier ones from the page (which this call does not
 // write), so it needs nothing from the copy blocks; theirs is the longer chain, so they come
-// first in the grid. 8191 tokens x 8 heads x 128 out of 12 KB rows: 12.7 us for the rows alone
-// (5.3 TB/s; 81 % of the measured copy rate), 16.1 us with bounds. One fused pass (a block per
+// first in the grid. 8191 tokens x 8 heads x 128 out of 12 KB rows, six pools and inputs in turn
+// (407 MB): 12.5 us for the rows alone (5.4 TB/s; 82 % of the measured copy rate), 15.9 us with
+// bounds (7.8 and 12.1 us out of L2, one pool again and again). One fused pass (a block per
 // page and two heads, extremes kept while copying) took 20.2 us: it reads the input's wide rows
 // in 512-byte pieces at different times.
 #include "kvs_device.cuh"

@@ -18,14 +18,22 @@
 // one partial per CTA in L2 (two slots a CTA: the unit it ends and the unit it begins). Short
 // shares are rounded to whole CTAs per unit, and where every unit is short and has a CTA of its
 // own, it is not split across CTAs at all (launch_paged).
-// K and V are read once and marked evict-first in L2 (64K-token decode 122 -> 120.5 us).
+// A call reads K and V once, and its copies are marked evict-first in L2. That gains where the
+// next call reads another cache, and costs where calls read one cache again and again (layers
+// that share a slot) and it fits L2 (bf16; evict-first against the normal policy):
+//   32 requests of up to 2K, 24 caches of 28 MB in turn:      13.2 against 13.9 us
+//   7 of up to 8K, 4 caches of 82 MB in turn:                 22.2 against 23.2 us
+//   the same, each cache read twice in a row:                 20.8 against 21.6 us
+//   one cache of 82 MB again and again:                       22.1 against 19.8 us
+//   32 of 2K, one cache of 67 MB again and again:             15.3 against 13.0 us
+//   4 of up to 64K, 746 MB:                                   116 to 118 us either way
 //
-// Measured (one layer, replayed back to back; DRAM reads equal the algorithmic bytes):
-//   4 requests of up to 64K tokens, 8 kv heads x 128, bf16:  119 us, 6.5 TB/s (99 % of the
-//                                                             measured copy rate)
+// Measured (one layer; graphs that go through several caches, 400 MB and more together):
+//   4 requests of up to 64K tokens, 8 kv heads x 128, bf16:  119 to 122 us, 6.3 to 6.5 TB/s (96 to
+//                                                             99 % of the measured copy rate)
 //   16 requests of up to 8K, two sources, 4 x 128, bf16:      55 us, 5.6 TB/s
-//   32 requests of up to 2K, 4 x 64, bf16:                    13.3 us, 2.7 TB/s
-//   one request of 320 tokens, 4 x 128, bf16:                 6.5 us
+//   32 requests of up to 2K, 4 x 64, bf16:                    13.6 us, 2.6 TB/s (12.3 out of L2)
+//   one request of 320 tokens, 4 x 128, bf16:                 6.4 us
 // Short calls are bound by the chain launch (2 us) -> lengths -> block table -> first tile (3 us
 // together) -> last tile -> joins (3 to 4 us), not by bytes.
 //
@@ -562,8 +570,11 @@ cudaError_t launch_paged(const CUtensorMap& tmK, const CUtensorMap& tmV, const P
     if (e != cudaSuccess) return e;
     // One CTA per unit where the units fit the grid and even the longest possible one is short:
     // joining a unit across CTAs costs about as much as 4 tiles of every warp. With most of the
-    // multiprocessors busy anyway twice that is worth it (one 320-token request: 8.8 -> 7.0 us;
-    // 32 ragged requests of up to 2K: 15.4 -> 14.8 us; but 8 units of 1K tokens: 19.2 -> 22.0 us).
+    // multiprocessors busy anyway twice that is worth it. Against the splits of the line (the
+    // caches together larger than L2): one 320-token request 7.7 -> 6.5 us; 16 requests of 500
+    // tokens, 4 x 128: 11.3 -> 8.9; 32 ragged ones of up to 2K, 4 x 64: 15.8 -> 13.2; 32 of 2K:
+    // 16.9 -> 15.3; 2 of 1K: 8.5 -> 7.7. Longer units on a CTA each lose (8 units of 1K tokens at
+    // 8 tiles a warp: 19.2 -> 22.0, measured on an earlier build).
     PagedDecodeArgs args = a;
     const int units = a.B * a.Hkv;
     const long long cap = static_cast<long long>(a.sel != nullptr ? std::min(a.top, a.max_blocks) : a.max_blocks) << a.page_shift;

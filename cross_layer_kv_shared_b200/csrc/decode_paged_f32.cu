@@ -5,10 +5,12 @@
 //   softmax of those heads, the weights written to shared memory
 //   output: lane = four channels (at d = 64 the half warps take alternate tokens); the weights
 //           of a token are read as broadcasts
-// 128-byte swizzled tiles keep every 16-byte read of K and V free of bank conflicts. Groups of up
-// to 4 stream near HBM speed (4 requests of up to 32K tokens, 4 x 128: 64.7 us, 87 % of the
-// measured copy rate); at 8 and 16 the two warps that a scheduler has wait on their own chains
-// of reads and multiply-adds (32 us where HBM needs 14, 8K tokens; 55 us for 7, 4K tokens).
+// 128-byte swizzled tiles keep every 16-byte read of K and V free of bank conflicts. 16 requests of
+// 4K to 8K tokens, 4 kv heads, share of the measured copy rate by group size (d 64, d 64 two
+// sources, d 128, d 128 two sources): up to 4 heads 82, 93, 92, 97 %; 8 heads 63, 81, 74, 59 %;
+// 16 heads 41, 31, 27, 33 %. At 8 and 16 the one or two warps that a scheduler has wait on their
+// own chains of reads and multiply-adds; short calls lose more (32 us where HBM needs 14, 8 heads,
+// 8K tokens; 55 us for 7, 16 heads, 4K tokens).
 // Tensor cores with tf32 operands in two parts were hardly faster (30 and 45 us) and lost
 // precision (1.5e-6 against 3e-7); paired multiply-adds gained 4 % and spilled at 16.
 #include "decode_paged.cuh"
