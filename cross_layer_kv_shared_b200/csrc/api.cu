@@ -839,7 +839,9 @@ kvshare_status kvshare_append_lowrank(kvshare_t ctx, const kvshare_cache* cache,
 kvshare_status kvshare_sync_status(kvshare_t ctx, void* stream) {
     if (ctx == nullptr) return KVS_EINVAL;
     if (cudaSetDevice(ctx->device) != cudaSuccess) return KVS_ECUDA;
-    if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return KVS_ECUDA;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (cudaStreamSynchronize(st) != cudaSuccess) return KVS_ECUDA;
+    static_assert((ERR_TIMEOUT | ERR_RANGE | ERR_POOL) <= 0xffu, "the word's low byte holds every fault");
     unsigned word = 0;
     if (cudaMemcpy(&word, ctx->err, sizeof(unsigned), cudaMemcpyDeviceToHost) != cudaSuccess) return KVS_ECUDA;
     // one kind of fault a call: the others stay recorded for the next ones
@@ -848,7 +850,10 @@ kvshare_status kvshare_sync_status(kvshare_t ctx, void* stream) {
     for (const auto& k : kinds) {
         if (!(word & k.bit)) continue;
         word &= ~k.bit;
-        if (cudaMemcpy(ctx->err, &word, sizeof(unsigned), cudaMemcpyHostToDevice) != cudaSuccess) return KVS_ECUDA;
+        // on the caller's stream and waited for: a kernel of the next call, on whatever stream, reports after it
+        if (cudaMemsetAsync(ctx->err, static_cast<int>(word), 1, st) != cudaSuccess ||
+            cudaStreamSynchronize(st) != cudaSuccess)
+            return KVS_ECUDA;
         return k.status;
     }
     return KVS_OK;
