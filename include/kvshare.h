@@ -344,8 +344,11 @@ kvshare_status kvshare_plan_pages(kvshare_t ctx, const int* lengths, const int* 
  * rows 0 .. the last one written here: per channel the largest and the smallest key,
  * rounded outwards to int8 with one fp32 scale per page and head (max |bound| * (1/127),
  * the reciprocal in fp32; codes ceil(hi / scale), floor(lo / scale) clamped to +-127). Keys
- * must be finite then. The tokens of one page must be consecutive, in row order (as
- * kvshare_plan_pages lays them out), and no slot may appear twice.
+ * must be finite then, and the rows written to one page must be consecutive rows that
+ * consecutive entries of slot_map name in order, with no skipped entry between them (as
+ * kvshare_plan_pages lays them out): a page written otherwise gets its rows, but bounds that
+ * may miss some of them. Without bounds the entries may come in any order. No slot may
+ * appear twice.
  * pages.block_table and lengths are not read. A decode that follows on the same stream
  * sees the new tokens. */
 kvshare_status kvshare_append_paged(kvshare_t ctx, const kvshare_pages* pages, int slot, const void* k_new,
