@@ -97,7 +97,8 @@ __global__ void __launch_bounds__(NT) plan_pages_kernel(const PagePlanArgs a) {
             const int m = a.new_tokens[b];
             if (len < 0 || len > cap) {
                 err |= ERR_RANGE;
-                len = m < 0 || len < 0 ? 0 : static_cast<int>(cap);   // which pages such a sequence holds is unknown: none returns
+                // which pages such a sequence holds is unknown: none returns
+                len = m < 0 || len < 0 ? 0 : static_cast<int>(cap);
             }
             n[e] = len;
             held[e] = (len + ps - 1) >> a.page_shift;
@@ -212,7 +213,8 @@ __global__ void __launch_bounds__(NT) plan_pages_kernel(const PagePlanArgs a) {
             int* entry = a.table + static_cast<size_t>(lo) * a.max_blocks + blk;
             const int page = k < 0 ? *entry : a.ring[ring_at(s_new[lo] + k)];
             if (k >= 0 && (pos & (ps - 1)) == 0) *entry = page;
-            // a page the pool does not have: no slot. Its product with the page size could wrap to another page's row
+            // a page the pool does not have gets no slot: its product with the page size could wrap
+            // to another page's row
             if (exists(page)) slot = page * ps + (pos & (ps - 1));
         }
         a.slot_map[i] = slot;

@@ -307,8 +307,8 @@ kvshare_status kvshare_append_lowrank(kvshare_t ctx, const kvshare_cache* cache,
  *   block_table [batch][max_blocks], in place: entries of new blocks are written
  *   ring        [num_pages] free pages, in place: `count` of them from entry `head` on,
  *               modulo num_pages; ring_state = {head, count}, 0 <= head < num_pages, 0 <= count
- *               <= num_pages (any other state is an empty ring without room and is reported as
- *               KVS_EINVAL)
+ *               <= num_pages (any other state is an empty ring without room, {0, 0} afterwards, and is
+ *               reported as KVS_EINVAL)
  *   lengths_out [batch]: n_b + m_b, or 0 for a sequence that leaves
  *   ring_state_out [2]; token_start [batch + 1]: first new token of each sequence, then
  *               their total
@@ -362,9 +362,10 @@ kvshare_status kvshare_append_paged(kvshare_t ctx, const kvshare_pages* pages, i
  *                row are used, in any order; one outside the sequence's blocks is skipped
  *                and reported as KVS_EINVAL; later entries may be anything), or NULL: every
  *                block
- * Sequences of any mix of lengths share the GPU evenly: the split is computed on the
- * device from the lengths, and the joins run in a fixed order, so the same inputs give the
- * same bits. Attention weights enter the P.V product with 24 bits: results differ from
+ * The split is computed on the device from the lengths, so that long sequences of any mix
+ * of lengths share the GPU evenly; where a row of the block table is short and there is a CTA
+ * for every sequence and kv head, each of these has one to itself. The joins run in a fixed
+ * order, so the same inputs give the same bits. Attention weights enter the P.V product with 24 bits: results differ from
  * exact arithmetic by fp32 rounding only. A sequence of length 0 gets out 0 and lse -inf.
  * LOWRANK layers: KVS_EUNSUPPORTED (their code groups are not paged). */
 kvshare_status kvshare_decode_paged(kvshare_t ctx, const kvshare_pages* pages, const void* q, float* out,
