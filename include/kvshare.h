@@ -365,8 +365,9 @@ kvshare_status kvshare_append_paged(kvshare_t ctx, const kvshare_pages* pages, i
  * The split is computed on the device from the lengths, so that long sequences of any mix
  * of lengths share the GPU evenly; where a row of the block table is short and there is a CTA
  * for every sequence and kv head, each of these has one to itself. The joins run in a fixed
- * order, so the same inputs give the same bits. Attention weights enter the P.V product with 24 bits: results differ from
- * exact arithmetic by fp32 rounding only. A sequence of length 0 gets out 0 and lse -inf.
+ * order, so the same inputs give the same bits. Attention weights enter the P.V product with
+ * 24 bits: results differ from exact arithmetic by fp32 rounding only. A sequence of length 0
+ * gets out 0 and lse -inf.
  * LOWRANK layers: KVS_EUNSUPPORTED (their code groups are not paged). */
 kvshare_status kvshare_decode_paged(kvshare_t ctx, const kvshare_pages* pages, const void* q, float* out,
                                     float* lse, const int* selected, int top, int l0, int l1, void* stream);
